@@ -76,6 +76,10 @@ typedef enum {
 #define VX_DATA_BAD_SEQ_LEN 2u   /* seq_lens[b] < 1 or > max_pages * page_size */
 #define VX_DATA_BAD_SELECTION 4u /* sel entry >= n_b (entries < 0 are empty slots) */
 #define VX_DATA_TIMEOUT 8u       /* a bounded wait inside a kernel ran out */
+#define VX_DATA_BAD_VALUE 16u    /* a new key or value is infinite or NaN (vx_quant_update) */
+#define VX_DATA_BAD_ROW 32u      /* a parent row or a new row's place out of range (vx_update_table) */
+#define VX_DATA_NO_PAGES 64u     /* fewer free pages than the new rows need (vx_update_table) */
+#define VX_DATA_BAD_COPY 128u    /* a destination named twice, or a source too (vx_copy_pages) */
 
 typedef struct {
     int32_t batch;         /* 1 <= B <= 4096 */
@@ -94,6 +98,20 @@ typedef struct {
     const int32_t *seq_lens;     /* [B] valid tokens, 1 <= seq_lens[b] <= max_pages * P */
     int32_t max_pages;           /* host bound on n_b over the batch; sizes scores rows */
 } vx_page_table;
+
+/*
+ * A cache held in 8 bits with one scale for each page and KV head (no counterpart in the
+ * paper note): element = code * scale.  GQA geometry only (MLA: VX_ERR_UNSUPPORTED).
+ */
+#define VX_QUANT_INT8 1 /* codes are int8 */
+#define VX_QUANT_E4M3 2 /* codes are fp8 e4m3 (no infinities, largest value 448) */
+typedef struct {
+    int32_t format; /* VX_QUANT_INT8 or VX_QUANT_E4M3, K and V alike */
+    void *k_cache;  /* [num_pool_pages][num_kv_heads][page_size][head_dim_qk] codes */
+    void *v_cache;  /* [num_pool_pages][num_kv_heads][page_size][head_dim_v] codes */
+    float *k_scale; /* [num_pool_pages][num_kv_heads] */
+    float *v_scale; /* [num_pool_pages][num_kv_heads] */
+} vx_quant_cache;
 
 /*
  * Cache stage: key centroid of a page = mean of the keys of its valid tokens, per KV
@@ -296,6 +314,156 @@ vx_status vx_sparse_decode_noalloc(const vx_geometry *geo, const vx_page_table *
                                    const void *k_cache, const void *v_cache, const int32_t *sel,
                                    int32_t k, float sm_scale, int32_t num_splits, void *out,
                                    float *lse, int32_t *err, void *stream);
+
+/*
+ * Cache stage of an 8-bit cache: quantise new tokens into their pages and recompute the
+ * centroids of the pages they touch, in one pass.  No counterpart in the paper note; the
+ * append and the prefill write of vx_centroid_update, for a vx_quant_cache.
+ *   first_pos == NULL: append one token per request (k_new, v_new [B][Hkv][D], bf16).
+ *   first_pos != NULL: prefill write, k_new and v_new [N][Hkv][D] packed in request order.
+ * Positions, tables and errors are those of vx_centroid_update.
+ * Scale of a page and head: the smallest power of two s >= 2^-126 for which every token the
+ * page holds has |x| <= qmax * s (qmax 127 or 448).  A token written into slot 0 starts a
+ * page: its old scale is forgotten.  Later tokens may raise the scale, never lower it; the
+ * codes already there are then divided by the factor and rounded once more (exact for e4m3
+ * down to its subnormals, at most half a step of the new scale for int8).  A scale found in a
+ * partly filled page may be any positive number (another program's): it is kept while it is
+ * large enough.
+ * code = x / s rounded to nearest, ties to even (s another program's: x * (1 / s)).
+ * Powers of two cost an int8 page up to one bit of its range (the mean is half a bit) and
+ * make every step reproducible: division by s is exact, so the code of a value depends on
+ * nothing but the value and s.
+ * A NaN is written as 0 and an infinity as bf16's largest finite value of its sign; both set
+ * VX_DATA_BAD_VALUE.
+ * Centroid: mean of the stored keys (code * scale) of the page's valid tokens, rounded once
+ * to bf16, so that the indexer scores what the attention reads.
+ * Writes: codes of the new tokens' slots (and of the page's older ones when its scale grows),
+ * the scales and the centroids of the pages touched.  Slots past a length are not written.
+ * Two requests that write into one page (a shared, partly filled one) race: fork such a page
+ * first (vx_update_table).
+ */
+vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, const vx_quant_cache *cache,
+                          void *centroids, const void *k_new, const void *v_new, const int32_t *first_pos,
+                          int32_t *err, void *stream);
+
+/*
+ * vx_sparse_decode over an 8-bit cache: the same arguments, selection, split plan, workspace
+ * and results, with K = k_code * k_scale and V = v_code * v_scale of each page and KV head.
+ * q and out stay bf16; logits, softmax statistics and sums are fp32.  Scales are any finite
+ * fp32 numbers (vx_quant_update makes powers of two).
+ */
+vx_status vx_sparse_decode_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
+                                 const vx_quant_cache *cache, const int32_t *sel, int32_t k, float sm_scale,
+                                 int32_t num_splits, void *out, float *lse, void *ws, size_t ws_bytes,
+                                 int32_t *err, void *stream);
+
+/*
+ * vx_block_topk_decode over an 8-bit cache: score -> top-k -> vx_sparse_decode_quant on one
+ * stream.  Arguments and results as there.
+ */
+vx_status vx_block_topk_decode_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
+                                     const vx_quant_cache *cache, const void *centroids, int32_t k, int32_t mode,
+                                     uint64_t seed, float sm_scale, int32_t score_dims, int32_t num_splits,
+                                     void *out, float *lse, float *scores_out, int32_t *sel_out, void *ws,
+                                     size_t ws_bytes, int32_t *err, void *stream);
+
+/*
+ * vx_block_topk_decode_append over an 8-bit cache: vx_quant_update's append (k_new, v_new
+ * [B][Hkv][D], required) -> score -> top-k -> vx_sparse_decode_quant.
+ */
+vx_status vx_block_topk_decode_append_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
+                                            const vx_quant_cache *cache, void *centroids, const void *k_new,
+                                            const void *v_new, int32_t k, int32_t mode, uint64_t seed, float sm_scale,
+                                            int32_t score_dims, int32_t num_splits, void *out, float *lse,
+                                            float *scores_out, int32_t *sel_out, void *ws, size_t ws_bytes,
+                                            int32_t *err, void *stream);
+
+/*
+ * Pages of a pool (no counterpart in the paper note: the part of a serving engine that hands
+ * out, shares, copies, frees and moves pages, on the device).
+ * A pool is a set of arrays with one entry per physical page, which move together: k_cache,
+ * v_cache (NULL for MLA), and where not NULL the centroids and the scales of an 8-bit cache.
+ * ref[p] counts the references to page p: one for each place in the rows of the page table
+ * that names it, plus the caller's own (a prefix cache).  A page is free when ref[p] == 0.
+ * Rows may be empty here (seq_lens[b] == 0).
+ * The three calls below are stream-ordered, read nothing on the host and are repeatable: the
+ * same inputs give the same pages.  ws: vx_page_workspace_size bytes, no initial contents
+ * needed; calls that share one are ordered on one stream.
+ */
+typedef struct {
+    void *k_cache;    /* [num_pages][num_kv_heads][page_size][head_dim_qk] */
+    void *v_cache;    /* [num_pages][num_kv_heads][page_size][head_dim_v]; NULL for MLA */
+    void *centroids;  /* [num_pages][num_kv_heads][head_dim_qk] bf16, or NULL */
+    float *k_scale;   /* [num_pages][num_kv_heads], or NULL (both scales or none; 8-bit caches only) */
+    float *v_scale;
+    int32_t elem_bytes; /* of k_cache and v_cache: 2 (bf16) or 1 (8-bit codes) */
+    int64_t num_pages;
+} vx_page_pool;
+
+/*
+ * Copy pages: for i < num_copies, page src_pages[i] of `src` to page dst_pages[i] of `dst`
+ * (device int32 arrays), all arrays of the pools.  Both pools have geo's page layout and the
+ * same arrays; `src` and `dst` may be one pool (the same k_cache).  dst->num_pages must be
+ * geo->num_pool_pages.  geo->batch is not used (but valid).
+ * A copy whose destination an earlier copy of the call names, or (in one pool) any copy names
+ * as a source, sets VX_DATA_BAD_COPY and is not made; one with a page outside its pool sets
+ * VX_DATA_BAD_PAGE_ID and is not made.  The others are.
+ */
+vx_status vx_copy_pages(const vx_geometry *geo, const vx_page_pool *src, const vx_page_pool *dst,
+                        const int32_t *src_pages, const int32_t *dst_pages, int32_t num_copies, void *ws,
+                        size_t ws_bytes, int32_t *err, void *stream);
+
+/*
+ * New rows of a page table from old ones: fork, reorder, free, grow and create rows in one
+ * call.  `table` holds the old rows (geo->batch of them); new row i < new_rows holds the
+ * tokens of old row parent[i] (parent[i] == -1: none) and room for grow[i] >= 0 more:
+ *   new_seq_lens[i] = (old length of parent[i], or 0) + grow[i].
+ * An old row that is nobody's parent is freed; one with several children is forked: whole
+ * pages are shared, a partly filled last page is kept by the row's first child (the lowest i)
+ * if it has no other reference (ref == 1), and copied to a fresh page for every other child,
+ * so that no two rows ever append into one page.  Fresh pages are the free pages of lowest
+ * id, handed to the new rows in order (in a row: the copy of the last page first).  Pages
+ * that this call frees are not handed out by it.
+ *   ref_in  [num_pool_pages]: references before the call.
+ *   ref_out [num_pool_pages]: references after it: ref_in, less the old rows' references, plus
+ *       the new rows'.  May be ref_in itself.
+ *   new_page_ptr [new_rows] (an input): start of row i in new_page_indices, which has
+ *       num_indices entries; rows must not overlap.  A row's entries past its pages are not
+ *       written.
+ *   new_page_indices, new_seq_lens: outputs, in memory of their own (not the old table's).
+ *   new_max_pages: bound on the pages of a new row, as vx_page_table.max_pages.
+ * All or nothing: when an old length, a parent, a growth, a new row's place or a forked last
+ * page's id is out of range, or the free pages do not suffice, the call sets the bit
+ * (VX_DATA_BAD_SEQ_LEN, _BAD_ROW, _BAD_PAGE_ID, _NO_PAGES), every new length to 0 and ref_out
+ * to ref_in, and touches neither the pool nor new_page_indices: the old rows are still good.
+ * Another old page id outside the pool sets VX_DATA_BAD_PAGE_ID; it is passed on to the new
+ * row and counted nowhere.
+ */
+vx_status vx_update_table(const vx_geometry *geo, const vx_page_pool *pool, const vx_page_table *table,
+                          const int32_t *ref_in, const int32_t *parent, const int32_t *grow, int32_t new_rows,
+                          const int32_t *new_page_ptr, int32_t *new_page_indices, int64_t num_indices,
+                          int32_t *new_seq_lens, int32_t new_max_pages, int32_t *ref_out, void *ws, size_t ws_bytes,
+                          int32_t *err, void *stream);
+
+/*
+ * Compact a pool: move every live page (ref > 0) with id >= n, n the number of live pages,
+ * into the free pages below n, lowest to lowest, so that the live pages are [0, n).
+ *   page_indices_out: the table's page_indices after the move (same offsets; only the entries
+ *       of rows' pages are written).  May be the table's own array.  Rows must not overlap.
+ *   ref_out [num_pool_pages]: references after the move.  May be ref_in itself.
+ *   remap [num_pool_pages]: new id of each live page, -1 for free ones (for references that
+ *       the caller holds outside the table).
+ *   num_live: n (one int32).
+ * A row with a length out of range sets VX_DATA_BAD_SEQ_LEN and keeps its entries; an entry
+ * outside the pool, or naming a free page, sets VX_DATA_BAD_PAGE_ID and is kept as it is.
+ */
+vx_status vx_compact_pages(const vx_geometry *geo, const vx_page_pool *pool, const vx_page_table *table,
+                           const int32_t *ref_in, int32_t *page_indices_out, int32_t *ref_out, int32_t *remap,
+                           int32_t *num_live, void *ws, size_t ws_bytes, int32_t *err, void *stream);
+
+/* Workspace bytes of the three page calls for pools of geo->num_pool_pages pages and at most
+ * `rows` new rows; 0 when the arguments are invalid (see vx_last_error). */
+size_t vx_page_workspace_size(const vx_geometry *geo, int32_t rows);
 
 /*
  * Workspace bytes that vx_sparse_decode and vx_block_topk_decode need for this geometry,

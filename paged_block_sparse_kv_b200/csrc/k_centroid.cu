@@ -15,31 +15,6 @@
 
 namespace vx {
 
-// Round a double to the nearest bf16, ties to even, directly from the double.
-__device__ __forceinline__ uint16_t f64_to_bf16_rne(double x) {
-    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
-    const uint16_t sign = static_cast<uint16_t>((u >> 48) & 0x8000u);
-    const int ebits = static_cast<int>((u >> 52) & 0x7ff);
-    if (ebits == 0x7ff) return (u & 0xfffffffffffffull) ? uint16_t(0x7fc0) : uint16_t(sign | 0x7f80);
-    const double ax = fabs(x);
-    if (ax == 0.0) return sign;
-    const int e = ebits - 1023;  // ax in [2^e, 2^(e+1)) for normal doubles (ours always are)
-    if (e < -126) {
-        // bf16 subnormal range: spacing 2^-133
-        const long long q = __double2ll_rn(ax * 0x1p133);  // exact scaling, RNE to integer
-        return static_cast<uint16_t>(sign | static_cast<uint16_t>(q));  // q == 128 -> min normal
-    }
-    // 8 significant bits: scale into [128, 256) and round to an integer, ties to even
-    long long q = __double2ll_rn(scalbn(ax, 7 - e));
-    int ee = e;
-    if (q == 256) {
-        q = 128;
-        ++ee;
-    }
-    if (ee > 127) return static_cast<uint16_t>(sign | 0x7f80);
-    return static_cast<uint16_t>(sign | ((ee + 127) << 7) | (static_cast<int>(q) & 0x7f));
-}
-
 // Centroid of rows [0, m) of one (page, head) block of D bf16 each, written to `dst`.
 // If alt != nullptr, row alt_slot is read from alt instead of the block (the token being
 // appended, not yet visible in the cache to this warp).
@@ -173,13 +148,6 @@ __global__ void k_centroid_append(CentroidArgs a) {
     }
     centroid_warp<D>(kc + blk * a.P * D, slot + 1, kn, slot,
                      static_cast<__nv_bfloat16 *>(a.centroids) + blk * D, lane);
-}
-
-// New tokens request i writes in a prefill: seq_lens[i] - first_pos[i], or none for a request
-// whose length or first position is out of range (reported by its own blocks).
-__device__ __forceinline__ int64_t prefill_count(const CentroidArgs &a, int i) {
-    const int32_t L = a.seq_lens[i], fp = a.first_pos[i];
-    return (L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L) ? (int64_t)(L - fp) : 0;
 }
 
 // One (page, head) of a prefill: rows [first_new, m) come from the packed input (new_row(t))

@@ -48,39 +48,6 @@ struct TileMeta<false> {
     int32_t nvalid;
 };
 
-__device__ __forceinline__ Resolved resolve_unit(const DecodeArgs &a, int64_t u, int64_t u_end) {
-    Resolved rs{0, 0, 0, 0, false};
-    if (u >= u_end) return rs;
-    const int64_t r = u / a.units_per_row;
-    const int64_t rem = u - r * a.units_per_row;
-    const int i = static_cast<int>(rem / a.tiles_per_page);
-    const int sub = static_cast<int>(rem - (int64_t)i * a.tiles_per_page);
-    const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
-    rs.row = static_cast<int32_t>(r);
-    const int32_t L = a.seq_lens[b];
-    if (L < 1 || L > a.max_pages * a.P) return rs;  // reported by the top-k kernel
-    const int32_t j = a.sel[r * a.k + i];
-    if (j < 0) return rs;
-    const int n = ceil_div(L, a.P);
-    if (j >= n) {
-        set_err(a.err, VX_DATA_BAD_SELECTION);
-        return rs;
-    }
-    const int tok0 = j * a.P + sub * DEC_TILE;
-    const int nvalid = min(DEC_TILE, L - tok0);
-    if (nvalid <= 0) return rs;
-    const int32_t phys = a.page_indices[a.page_ptr[b] + j];
-    if (phys < 0 || phys >= a.num_pool_pages) {
-        set_err(a.err, VX_DATA_BAD_PAGE_ID);
-        return rs;
-    }
-    rs.z = phys * a.Hkv + h;
-    rs.y = sub * DEC_TILE;
-    rs.nvalid = nvalid;
-    rs.valid = true;
-    return rs;
-}
-
 // LATE: the split has late pieces (a.chunks > a.static_chunks).  Without them a warp's static
 // piece is all it does and the kernel runs the plain one-chunk-per-warp loop (the piece
 // bookkeeping cost the headline and long-context steps 0.4-2 us when compiled in).

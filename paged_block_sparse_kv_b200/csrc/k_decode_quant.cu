@@ -1,0 +1,452 @@
+// k_decode_quant.cu -- exact softmax attention over the selected pages of an 8-bit cache (GQA).
+//
+// For query head g of KV head h, over the valid tokens t of the selected pages p:
+//   x_t = sm_scale * k_scale[p][h] * (q_g . kc_t),  out = sum_t softmax(x)_t v_scale[p][h] vc_t
+// with kc, vc the codes (int8 or e4m3).  The work split (flat list of 16-token tiles, pieces,
+// one partial per (row, piece), merge) is that of k_decode.cu, whose merge kernel is used.
+//
+// Both code types are exact in fp16 (int8: integers up to 128; e4m3: 4 significant bits,
+// 2^-9 .. 448), so the products run as fp16 mma with fp32 sums and the scales stay outside:
+// k_scale multiplies a tile's logits, v_scale a tile's P.V product.  The query is bf16, whose
+// range fp16 lacks: each query head is first scaled by a power of two that puts its largest
+// element into [2^14, 2^15), exact for every element down to 2^-29 of the largest (smaller
+// ones keep an absolute error of 2^-40 of it), and the factor goes into the logits' scale.  P
+// is rounded to fp16, to half a step of 2^-10 where bf16's is 2^-7; it is taken relative to
+// 2^-DQ_PSHIFT of the running maximum, so that weights down to 2^-29 are normal numbers.
+//
+// Fragments straight from 8-bit tiles, no transposition of bytes:
+//  * K (A operand, tokens x dims): the order of the contracted dims is free as long as Q has
+//    the same one, so a lane takes 16 consecutive dims of its two token rows with one 16-byte
+//    shared load each and feeds 4 mma steps from them (bytes 4s, 4s+1 and 4s+2, 4s+3 are the
+//    two k halves of step s).
+//  * V (A operand, dims x tokens): ldmatrix.trans moves byte pairs, so a lane gets two dims
+//    of two tokens per register: bytes 0, 2 are dim 2g of both tokens, bytes 1, 3 dim 2g + 1.
+//    Row g of the fragment is dim 2g of the 16, row g + 8 dim 2g + 1; nothing else changes.
+// Value codes past the request's length are zeroed in registers, logits there are -inf.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "vx_attend.cuh"
+
+namespace vx {
+
+namespace {
+
+constexpr float DQ_PSHIFT = 15.f;  // weights are at most 2^15, fp16's largest number is 65504
+constexpr int DQ_STAGES = 6;  // 16-token tiles in flight per warp (4 KB each at head_dim 128)
+
+struct QuantMeta {
+    int32_t row, nvalid, piece;
+    float ks, vs;
+};
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+
+// D = A(16x16, row) * B(16x8, col) + D, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four codes to fp16: bytes (0, 1) and (2, 3) of w, or (0, 2) and (1, 3) when SPLIT.
+template <int FMT, bool SPLIT>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == VX_QUANT_INT8) {
+        // u = code + 128 as the low byte of fp16 1024 + u; less 1152 gives the code, exactly
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+        const uint32_t a = __byte_perm(u, 0x64646464u, SPLIT ? 0x4240 : 0x4140);
+        const uint32_t b = __byte_perm(u, 0x64646464u, SPLIT ? 0x4341 : 0x4342);
+        lo = half2_bits(__hsub2(*reinterpret_cast<const __half2 *>(&a), off));
+        hi = half2_bits(__hsub2(*reinterpret_cast<const __half2 *>(&b), off));
+    } else {
+        const uint32_t v = SPLIT ? __byte_perm(w, 0u, 0x3120) : w;
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> 16), __NV_E4M3);
+        lo = half2_bits(__half2(a));
+        hi = half2_bits(__half2(b));
+    }
+}
+
+// Byte offset of 16-byte chunk `chunk` of token row `row` in a tile: rows of D bytes, swizzled
+// by TMA over 128 bytes (D = 128) or 64 bytes (D = 64, where the pattern repeats every 8 rows).
+template <int D>
+__device__ __forceinline__ uint32_t code_off(int row, int chunk) {
+    if constexpr (D == 128) return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+    return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// One 16-token tile.  qf: the query heads as mma B fragments in the dims order above; hs: the
+// logits' scale of heads 2 q4, 2 q4 + 1 (log2 units); acc: unnormalised output.
+template <int D, int NT, int FMT>
+__device__ __forceinline__ void attend_codes(uint32_t sK, uint32_t sV, int nvalid, float ks, float vs,
+                                             const uint32_t (&qf)[NT][D / 16][2], const float (&hs)[NT][2],
+                                             float (&acc)[NT][D / 16][4], float (&m_run)[NT][2],
+                                             float (&l_run)[NT][2], int lane) {
+    constexpr int MT = D / 16;
+    constexpr int HALVES = D / 64;  // 16-byte chunks a lane takes of a token row
+    const int g4 = lane >> 2, q4 = lane & 3;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+        // chunk HALVES * q4 + h: the 8 lanes of a quarter warp cover all 32 banks
+        const uint4 r0 = lds_v4(sK + code_off<D>(g4, HALVES * q4 + h));
+        const uint4 r1 = lds_v4(sK + code_off<D>(g4 + 8, HALVES * q4 + h));
+        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_half<FMT, false>(w0[st], a0, a2);
+            codes_to_half<FMT, false>(w1[st], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][h * 4 + st][0], qf[nt][h * 4 + st][1]);
+        }
+    }
+    // online softmax (base 2), tokens >= nvalid masked
+    uint32_t pb[NT][2];
+    float alpha[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int tok = g4 + 8 * (e >> 1);
+            x[e] = tok < nvalid ? s[nt][e] * (hs[nt][e & 1] * ks) : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(x[i], x[i + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
+            const float m_new = fmaxf(m_run[nt][i], mx);
+            alpha[nt][i] = exp2f(m_run[nt][i] - m_new);
+            m_run[nt][i] = m_new;
+        }
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = exp2f(x[e] - (m_run[nt][e & 1] - DQ_PSHIFT));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) l_run[nt][i] = l_run[nt][i] * alpha[nt][i] + p[i] + p[i + 2];
+        pb[nt][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
+        pb[nt][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
+    }
+    // O^T[dim][head] = alpha * O^T + v_scale * (codes . P^T)
+    const int mi = lane >> 3, tok = (lane & 7) + 8 * (mi & 1);
+    const bool tail = nvalid < DEC_TILE;
+    const int t_lo = 2 * q4, t_hi = 8 + 2 * q4;  // tokens of this lane's A halves
+    const uint32_t mlo = (t_lo < nvalid ? 0x0000ffffu : 0u) | (t_lo + 1 < nvalid ? 0xffff0000u : 0u);
+    const uint32_t mhi = (t_hi < nvalid ? 0x0000ffffu : 0u) | (t_hi + 1 < nvalid ? 0xffff0000u : 0u);
+#pragma unroll
+    for (int c = 0; c < MT; c += 2) {
+        uint32_t r[4];
+        ldsm_x4_t(sV + code_off<D>(tok, c + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t lo = r[2 * u], hi = r[2 * u + 1];
+            if (tail) {
+                lo &= mlo;
+                hi &= mhi;
+            }
+            uint32_t a0, a1, a2, a3;
+            codes_to_half<FMT, true>(lo, a0, a1);
+            codes_to_half<FMT, true>(hi, a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16_16816(d, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][c + u][e] = fmaf(vs, d[e], acc[nt][c + u][e] * alpha[nt][e & 1]);
+            }
+        }
+    }
+}
+
+// LATE: the split has late pieces (see k_decode.cu).
+template <int D, int NT, int FMT, bool LATE>
+__global__ void __launch_bounds__(DEC_WARPS * 32, 1)
+    k_decode_quant(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const DecodeArgs a, const float *__restrict__ k_scale, const float *__restrict__ v_scale) {
+    constexpr int TILE_BYTES = DEC_TILE * D;
+    constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K tile + V tile
+    constexpr int MT = D / 16;
+    constexpr int HALVES = D / 64;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle wants 1 KB alignment
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g4 = lane >> 2, q4 = lane & 3;
+    const uint32_t stage0 = base + (uint32_t)(warp * DQ_STAGES) * STAGE_BYTES;
+    const uint32_t bar0 = base + (uint32_t)(DEC_WARPS * DQ_STAGES) * STAGE_BYTES + (uint32_t)(warp * DQ_STAGES) * 8u;
+    QuantMeta *meta = reinterpret_cast<QuantMeta *>(smem_raw + (base - raw) + DEC_WARPS * DQ_STAGES * STAGE_BYTES +
+                                                    DEC_WARPS * DQ_STAGES * 8) +
+                      warp * DQ_STAGES;
+
+    if (lane == 0) {
+        for (int s = 0; s < DQ_STAGES; ++s) mbar_init(bar0 + 8u * s, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    __syncwarp();
+
+    const int64_t wid = (int64_t)blockIdx.x * DEC_WARPS + warp;
+    if (wid >= a.static_chunks) return;
+
+    uint32_t qf[NT][MT][2];
+    float hs[NT][2];
+    float acc[NT][MT][4];
+    float m_run[NT][2], l_run[NT][2];
+
+    // partial of row `r` (at least one tile attended) for piece `c`: slot r + c
+    auto write_partial = [&](int64_t r, int64_t c) {
+        const int64_t slot = r + c;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int head = nt * 8 + 2 * q4 + i;
+                float v = l_run[nt][i];
+                v += __shfl_xor_sync(FULL, v, 4);
+                v += __shfl_xor_sync(FULL, v, 8);
+                v += __shfl_xor_sync(FULL, v, 16);
+                if (head < a.G) {
+                    float *o = a.o_part + (slot * a.G + head) * D + 2 * g4;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i], acc[nt][mt][2 + i]);
+                    if (g4 == 0) {
+                        float *ml = a.ml_part + (slot * a.G + head) * 2;
+                        ml[0] = m_run[nt][i] - DQ_PSHIFT;  // what the weights are relative to
+                        ml[1] = v;
+                    }
+                }
+            }
+    };
+    auto start_row = [&](int64_t r) {
+        const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
+        const __nv_bfloat16 *qb = a.q + ((size_t)b * a.Hq + (size_t)h * a.G) * D;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int head = nt * 8 + g4;
+            uint2 w[MT];  // dims (HALVES q4 + half) 16 + 4 st .. + 3 of step half * 4 + st
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                w[i] = make_uint2(0u, 0u);
+                if (head < a.G)
+                    w[i] = *reinterpret_cast<const uint2 *>(qb + (size_t)head * D + (HALVES * q4 + i / 4) * 16 + (i & 3) * 4);
+                top = __vmaxu2(top, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+            }
+            uint32_t amax = max(top & 0xffffu, top >> 16);
+            amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
+            amax = max(amax, __shfl_xor_sync(FULL, amax, 2));
+            // 2^(14 - exponent of the largest element), kept in fp32's normal range
+            const uint32_t ef = min(268u - (amax >> 7), 253u);
+            const float mul = __uint_as_float(ef << 23);
+            const float inv = __uint_as_float((254u - ef) << 23) * a.scale_log2;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                qf[nt][i][0] = half2_bits(__floats2half2_rn(__uint_as_float(w[i].x << 16) * mul,
+                                                            __uint_as_float(w[i].x & 0xffff0000u) * mul));
+                qf[nt][i][1] = half2_bits(__floats2half2_rn(__uint_as_float(w[i].y << 16) * mul,
+                                                            __uint_as_float(w[i].y & 0xffff0000u) * mul));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                hs[nt][i] = __shfl_sync(FULL, inv, (2 * q4 + i) * 4);
+                m_run[nt][i] = -INFINITY;
+                l_run[nt][i] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
+        }
+    };
+    auto p_start = [&](int64_t c) -> int64_t {
+        if constexpr (LATE) return piece_start(c, a.units, a.static_units, a.static_chunks, a.chunks);
+        return chunk_start(c, a.units, a.chunks);
+    };
+    // the next piece this warp takes after its static one (warp-uniform): from the counter, or
+    // round robin over the warps; a.chunks or more: none left
+    int64_t rr_next = a.static_chunks + wid;
+    auto next_piece = [&]() -> int64_t {
+        if constexpr (!LATE) return a.chunks;
+        if (a.piece_ctr) {
+            unsigned v = 0;
+            if (lane == 0) v = atomicAdd(a.piece_ctr, 1u);
+            return a.static_chunks + (int64_t)__shfl_sync(FULL, v, 0);
+        }
+        const int64_t c = rr_next;
+        rr_next += a.static_chunks;
+        return c;
+    };
+    // every row that a piece touches starts with an empty partial (max -inf, sum 0); rows with
+    // attended tiles get theirs overwritten later by this same warp
+    auto empty_piece = [&](int64_t c) {
+        const int64_t u0 = p_start(c), u1 = p_start(c + 1);
+        for (int64_t r = u0 / a.units_per_row; r <= (u1 - 1) / a.units_per_row; ++r)
+            if (lane < a.G) {
+                float *ml = a.ml_part + ((r + c) * a.G + lane) * 2;
+                ml[0] = -INFINITY;
+                ml[1] = 0.f;
+            }
+        __syncwarp();
+    };
+
+    int64_t fc = wid, batch = p_start(wid), f_end = p_start(wid + 1);
+    int64_t cur_row = batch / a.units_per_row, cur_pc = wid;  // (row, piece) being accumulated
+    bool attended = false;                                    // it has a tile
+    // the query is an input of the call, complete before this grid starts, and the workspace is
+    // not touched by the previous kernel: only the selection waits for it
+    start_row(cur_row);
+    empty_piece(fc);
+    pdl_wait();
+
+    Resolved rs;
+    float ks, vs;
+    auto resolve = [&]() {
+        rs = resolve_unit(a, batch + lane, f_end);
+        ks = vs = 0.f;
+        if (rs.valid) {
+            ks = __ldg(k_scale + rs.z);
+            vs = __ldg(v_scale + rs.z);
+        }
+        return __ballot_sync(FULL, rs.valid);
+    };
+    uint32_t pending = resolve();
+    uint32_t issued = 0, consumed = 0;
+    bool fill_done = false, failed = false;
+
+    for (;;) {
+        // issue loads until the ring is full or no piece is left
+        while (!failed && !fill_done && issued - consumed < DQ_STAGES) {
+            if (pending == 0) {
+                batch += 32;
+                if (batch >= f_end) {
+                    const int64_t c = next_piece();
+                    if (c >= a.chunks) {
+                        fill_done = true;
+                        break;
+                    }
+                    fc = c;
+                    batch = p_start(c);
+                    f_end = p_start(c + 1);
+                    empty_piece(c);
+                }
+                pending = resolve();
+                continue;
+            }
+            const int src = __ffs(pending) - 1;
+            pending &= pending - 1;
+            const int st = static_cast<int>(issued % DQ_STAGES);
+            if (lane == src) {
+                const uint32_t bar = bar0 + 8u * st;
+                const uint32_t dst = stage0 + (uint32_t)st * STAGE_BYTES;
+                // no proxy fence: this stage's earlier shared-memory reads have completed, their
+                // values were consumed before the __syncwarp that released the stage
+                mbar_arrive_expect_tx(bar, STAGE_BYTES);
+                tma_load_3d(dst, &tmK, 0, rs.y, rs.z, bar);
+                tma_load_3d(dst + TILE_BYTES, &tmV, 0, rs.y, rs.z, bar);
+                meta[st].row = rs.row;
+                meta[st].nvalid = rs.nvalid;
+                meta[st].piece = static_cast<int32_t>(fc);
+                meta[st].ks = ks;
+                meta[st].vs = vs;
+            }
+            __syncwarp();
+            ++issued;
+        }
+        // next tile, or the end (row -1)
+        int64_t row = -1, pc = -1;
+        int nvalid = 0, st = 0;
+        float tks = 0.f, tvs = 0.f;
+        if (!failed && consumed != issued) {
+            st = static_cast<int>(consumed % DQ_STAGES);
+            if (!__all_sync(FULL, mbar_wait_sleep(bar0 + 8u * st, (consumed / DQ_STAGES) & 1u))) {
+                // a load did not arrive in time: report, let every issued load land, drop the
+                // partial in progress (its slot keeps its empty partial) and give every piece
+                // this warp would still have taken its empty partials
+                if (lane == 0) set_err(a.err, VX_DATA_TIMEOUT);
+                for (uint32_t i = consumed; i < issued; ++i)
+                    (void)mbar_wait_bounded(bar0 + 8u * (i % DQ_STAGES), (i / DQ_STAGES) & 1u);
+                failed = true;
+                attended = false;
+                while (!fill_done) {
+                    const int64_t c = next_piece();
+                    if (c >= a.chunks) fill_done = true;
+                    else empty_piece(c);
+                }
+            } else {
+                row = meta[st].row;
+                pc = meta[st].piece;
+                nvalid = meta[st].nvalid;
+                tks = meta[st].ks;
+                tvs = meta[st].vs;
+            }
+        }
+        if (row != cur_row || pc != cur_pc) {
+            if (attended) write_partial(cur_row, cur_pc);
+            if (row < 0) break;
+            if (row != cur_row || attended) start_row(row);
+            cur_row = row;
+            cur_pc = pc;
+        }
+        const uint32_t sK = stage0 + (uint32_t)st * STAGE_BYTES;
+        attend_codes<D, NT, FMT>(sK, sK + TILE_BYTES, nvalid, tks, tvs, qf, hs, acc, m_run, l_run, lane);
+        attended = true;
+        __syncwarp();  // every lane is done with this stage before it is refilled
+        ++consumed;
+    }
+}
+
+template <int D, int NT, int FMT>
+cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                       int grid, cudaStream_t s, bool pdl) {
+    const size_t smem = 1024 + (size_t)DEC_WARPS * DQ_STAGES * (2 * DEC_TILE * D + 8 + sizeof(QuantMeta));
+    const bool late = a.chunks > a.static_chunks;
+    auto kern = late ? k_decode_quant<D, NT, FMT, true> : k_decode_quant<D, NT, FMT, false>;
+    static std::atomic<unsigned long long> done[2];
+    cudaError_t e = ensure_smem_limit(kern, (int)smem, done[late ? 1 : 0]);
+    if (e != cudaSuccess) return e;
+    return launch_k(kern, dim3(grid), dim3(DEC_WARPS * 32), smem, s, pdl, tmK, tmV, a, (const float *)qa.k_scale,
+                    (const float *)qa.v_scale);
+}
+
+template <int D, int NT>
+cudaError_t launch_dn(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                      int grid, cudaStream_t s, bool pdl) {
+    return qa.format == VX_QUANT_INT8 ? launch_dnf<D, NT, VX_QUANT_INT8>(a, qa, tmK, tmV, grid, s, pdl)
+                                      : launch_dnf<D, NT, VX_QUANT_E4M3>(a, qa, tmK, tmV, grid, s, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_quant(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK,
+                                const CUtensorMap &tmV, int grid, cudaStream_t s, bool pdl) {
+    const int nt = (a.G + 7) / 8;
+    if (a.Dqk == 128 && nt == 1) return launch_dn<128, 1>(a, qa, tmK, tmV, grid, s, pdl);
+    if (a.Dqk == 128 && nt == 2) return launch_dn<128, 2>(a, qa, tmK, tmV, grid, s, pdl);
+    if (a.Dqk == 64 && nt == 1) return launch_dn<64, 1>(a, qa, tmK, tmV, grid, s, pdl);
+    if (a.Dqk == 64 && nt == 2) return launch_dn<64, 2>(a, qa, tmK, tmV, grid, s, pdl);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace vx

@@ -330,14 +330,48 @@ vx_status make_cache_map_blocks(CUtensorMap *map, const void *ptr, int dim, int 
     return VX_OK;
 }
 
+// The codes of an 8-bit cache as (dim, page_size, page-heads), boxes of DEC_TILE token rows; 128- or
+// 64-byte swizzling by the row's size.
+vx_status make_code_map(CUtensorMap *map, const void *ptr, int dim, int page_size, int64_t page_heads) {
+    auto fn = encode_fn();
+    if (!fn) return fail(VX_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t gdim[3] = {(cuuint64_t)dim, (cuuint64_t)page_size, (cuuint64_t)page_heads};
+    cuuint64_t gstride[2] = {(cuuint64_t)dim, (cuuint64_t)dim * page_size};
+    cuuint32_t box[3] = {(cuuint32_t)dim, (cuuint32_t)vx::DEC_TILE, 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), gdim, gstride, box, estride,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(VX_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return VX_OK;
+}
+
+vx_status check_quant(const vx_geometry *g, const vx_quant_cache *c) {
+    if (!c) return fail(VX_ERR_INVALID_ARG, "quantised cache is NULL");
+    if (c->format != VX_QUANT_INT8 && c->format != VX_QUANT_E4M3)
+        return fail(VX_ERR_INVALID_ARG, "format %d must be VX_QUANT_INT8 or VX_QUANT_E4M3", c->format);
+    if (g->mla_shared_kv) return fail(VX_ERR_UNSUPPORTED, "8-bit caches are built for the GQA geometry only");
+    VX_TRY(check_ptr(c->k_cache, "k_cache"));
+    VX_TRY(check_ptr(c->v_cache, "v_cache"));
+    if (!c->k_scale || !c->v_scale || !al4(c->k_scale) || !al4(c->v_scale))
+        return fail(VX_ERR_INVALID_ARG, "k_scale and v_scale must be 4-byte aligned and not NULL");
+    return VX_OK;
+}
+
+vx::QuantArgs quant_args(const vx_quant_cache *c) {
+    return {static_cast<uint8_t *>(c->k_cache), static_cast<uint8_t *>(c->v_cache), c->k_scale, c->v_scale, c->format};
+}
+
 // ------------------------------------------------------------------ shared launch pieces
 
+// quant: NULL, or the 8-bit cache to read in place of k_cache and v_cache
 // piece_ctr: NULL, or a workspace word zeroed earlier on the stream (by the step's scorer or a
 // memset); late pieces are then handed out to whichever warp is free first
 vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q, const void *k_cache,
                     const void *v_cache, const int32_t *sel, int32_t k, float sm_scale, const Plan &p,
                     const WsLayout &l, void *ws, void *out, float *lse, int32_t *err, cudaStream_t s, bool pdl,
-                    uint32_t *piece_ctr = nullptr) {
+                    uint32_t *piece_ctr = nullptr, const vx_quant_cache *quant = nullptr) {
     vx::DecodeArgs a{};
     a.page_ptr = t->page_ptr;
     a.page_indices = t->page_indices;
@@ -370,7 +404,12 @@ vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q,
     a.scale_log2 = scale * 1.4426950408889634f;
     const int64_t page_heads = g->num_pool_pages * g->num_kv_heads;
     cudaError_t e;
-    if (p.mla) {
+    if (quant) {
+        CUtensorMap tmK, tmV;
+        VX_TRY(make_code_map(&tmK, quant->k_cache, g->head_dim_qk, g->page_size, page_heads));
+        VX_TRY(make_code_map(&tmV, quant->v_cache, g->head_dim_v, g->page_size, page_heads));
+        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.grid, s, pdl);
+    } else if (p.mla) {
         CUtensorMap tmK, tmQ;
         VX_TRY(make_cache_map_blocks(&tmK, k_cache, g->head_dim_qk, g->page_size, page_heads,
                                      g->page_size / p.tiles_per_page));
@@ -386,6 +425,31 @@ vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q,
     e = vx::launch_merge(a, s, true);
     if (e != cudaSuccess) return cuda_fail(e, "merge launch");
     return VX_OK;
+}
+
+vx::CentroidArgs centroid_args(const vx_geometry *g, const vx_page_table *t, void *k_cache, void *v_cache,
+                               void *centroids, const void *k_new, const void *v_new, const int32_t *first_pos,
+                               int32_t *err) {
+    vx::CentroidArgs a{};
+    a.page_ptr = t->page_ptr;
+    a.page_indices = t->page_indices;
+    a.seq_lens = t->seq_lens;
+    a.first_pos = first_pos;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.centroids = centroids;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.err = err;
+    a.B = g->batch;
+    a.Hkv = g->num_kv_heads;
+    a.Dqk = g->head_dim_qk;
+    a.Dv = g->head_dim_v;
+    a.P = g->page_size;
+    a.max_pages = t->max_pages;
+    a.mla_shared_kv = g->mla_shared_kv;
+    a.num_pool_pages = g->num_pool_pages;
+    return a;
 }
 
 vx::ScoreArgs score_args(const vx_geometry *g, const vx_page_table *t, const void *q, const void *centroids,
@@ -444,6 +508,14 @@ vx_status check_k_mode(int32_t k, int32_t mode) {
 }  // namespace
 
 namespace vx {
+
+vx_status validate_geometry(const vx_geometry *geo) { return check_geometry(geo); }
+vx_status validate_table(const vx_geometry *geo, const vx_page_table *table) { return check_geo(geo, table); }
+vx_status validate_ptr(const void *p, const char *name, bool can_be_null) { return check_ptr(p, name, can_be_null); }
+int current_sm_count() {
+    int n = 0;
+    return sm_count_current(&n) == 0 ? n : 0;
+}
 
 vx_status decode_partial_bytes(const vx_geometry *geo, int32_t max_pages, int32_t k, int32_t num_splits,
                                size_t *bytes) {
@@ -560,26 +632,9 @@ vx_status vx_centroid_update(const vx_geometry *geo, const vx_page_table *table,
     }
     if (first_pos && !al4(first_pos)) return fail(VX_ERR_INVALID_ARG, "first_pos must be 4-byte aligned");
     if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
-    vx::CentroidArgs a{};
-    a.page_ptr = table->page_ptr;
-    a.page_indices = table->page_indices;
-    a.seq_lens = table->seq_lens;
-    a.first_pos = mode == vx::CEN_APPEND ? nullptr : first_pos;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.centroids = centroids;
-    a.k_new = k_new;
-    a.v_new = v_new;
-    a.err = err;
-    a.B = geo->batch;
-    a.Hkv = geo->num_kv_heads;
-    a.Dqk = geo->head_dim_qk;
-    a.Dv = geo->head_dim_v;
-    a.P = geo->page_size;
-    a.max_pages = table->max_pages;
-    a.mla_shared_kv = geo->mla_shared_kv;
-    a.num_pool_pages = geo->num_pool_pages;
-    cudaError_t e = vx::launch_centroid(a, mode, static_cast<cudaStream_t>(stream));
+    cudaError_t e = vx::launch_centroid(centroid_args(geo, table, k_cache, v_cache, centroids, k_new, v_new,
+                                                      mode == vx::CEN_APPEND ? nullptr : first_pos, err),
+                                        mode, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "centroid launch");
     return VX_OK;
 }
@@ -611,13 +666,15 @@ vx_status vx_topk_pages(const vx_geometry *geo, const vx_page_table *table, cons
     return VX_OK;
 }
 
-vx_status vx_sparse_decode(const vx_geometry *geo, const vx_page_table *table, const void *q, const void *k_cache,
-                           const void *v_cache, const int32_t *sel, int32_t k, float sm_scale, int32_t num_splits,
-                           void *out, float *lse, void *ws, size_t ws_bytes, int32_t *err, void *stream) {
-    VX_TRY(check_geo(geo, table));
-    VX_TRY(check_ptr(q, "q"));
-    VX_TRY(check_ptr(k_cache, "k_cache"));
-    if (!geo->mla_shared_kv) VX_TRY(check_ptr(v_cache, "v_cache"));
+}  // extern "C"
+
+namespace {
+
+// vx_sparse_decode and, with `quant`, vx_sparse_decode_quant
+vx_status sparse_decode(const vx_geometry *geo, const vx_page_table *table, const void *q, const void *k_cache,
+                        const void *v_cache, const vx_quant_cache *quant, const int32_t *sel, int32_t k, float sm_scale,
+                        int32_t num_splits, void *out, float *lse, void *ws, size_t ws_bytes, int32_t *err,
+                        void *stream) {
     VX_TRY(check_ptr(sel, "sel"));
     VX_TRY(check_ptr(out, "out"));
     VX_TRY(check_ptr(lse, "lse", true));
@@ -637,25 +694,25 @@ vx_status vx_sparse_decode(const vx_geometry *geo, const vx_page_table *table, c
         const cudaError_t e = cudaMemsetAsync(dctr, 0, sizeof(uint32_t), s);
         if (e != cudaSuccess) return cuda_fail(e, "piece counter reset");
     }
-    return do_decode(geo, table, q, k_cache, v_cache, sel, k, sm_scale, p, l, ws, out, lse, err, s, false, dctr);
+    return do_decode(geo, table, q, k_cache, v_cache, sel, k, sm_scale, p, l, ws, out, lse, err, s, false, dctr, quant);
 }
-
-}  // extern "C"
-
-namespace {
 
 // The chained step score -> top-k -> decode -> merge; `append` (k_new non-NULL) first writes
 // each request's new token and recomputes its page's centroid, and the scorer then follows
-// with programmatic dependent launch.
+// with programmatic dependent launch.  `quant`: the cache is this one (k_cache, v_cache unused).
 vx_status fused_step(const vx_geometry *geo, const vx_page_table *table, const void *q, const void *k_cache,
-                     const void *v_cache, const void *centroids, void *k_cache_w, void *v_cache_w, void *centroids_w,
+                     const void *v_cache, const vx_quant_cache *quant, const void *centroids, void *k_cache_w, void *v_cache_w, void *centroids_w,
                      const void *k_new, const void *v_new, int32_t k, int32_t mode, uint64_t seed, float sm_scale,
                      int32_t score_dims, int32_t num_splits, void *out, float *lse, float *scores_out, int32_t *sel_out,
                      void *ws, size_t ws_bytes, int32_t *err, void *stream) {
     VX_TRY(check_geo(geo, table));
     VX_TRY(check_ptr(q, "q"));
-    VX_TRY(check_ptr(k_cache, "k_cache"));
-    if (!geo->mla_shared_kv) VX_TRY(check_ptr(v_cache, "v_cache"));
+    if (quant) {
+        VX_TRY(check_quant(geo, quant));
+    } else {
+        VX_TRY(check_ptr(k_cache, "k_cache"));
+        if (!geo->mla_shared_kv) VX_TRY(check_ptr(v_cache, "v_cache"));
+    }
     VX_TRY(check_ptr(centroids, "centroids"));
     VX_TRY(check_ptr(out, "out"));
     VX_TRY(check_ptr(lse, "lse", true));
@@ -682,26 +739,10 @@ vx_status fused_step(const vx_geometry *geo, const vx_page_table *table, const v
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (k_new) {
-        vx::CentroidArgs ca{};
-        ca.page_ptr = table->page_ptr;
-        ca.page_indices = table->page_indices;
-        ca.seq_lens = table->seq_lens;
-        ca.first_pos = nullptr;
-        ca.k_cache = k_cache_w;
-        ca.v_cache = v_cache_w;
-        ca.centroids = centroids_w;
-        ca.k_new = k_new;
-        ca.v_new = v_new;
-        ca.err = err;
-        ca.B = geo->batch;
-        ca.Hkv = geo->num_kv_heads;
-        ca.Dqk = geo->head_dim_qk;
-        ca.Dv = geo->head_dim_v;
-        ca.P = geo->page_size;
-        ca.max_pages = table->max_pages;
-        ca.mla_shared_kv = geo->mla_shared_kv;
-        ca.num_pool_pages = geo->num_pool_pages;
-        e = vx::launch_centroid(ca, vx::CEN_APPEND, s);
+        const vx::CentroidArgs ca =
+            centroid_args(geo, table, k_cache_w, v_cache_w, centroids_w, k_new, v_new, nullptr, err);
+        e = quant ? vx::launch_quant_update(ca, quant_args(quant), vx::CEN_APPEND, s)
+                  : vx::launch_centroid(ca, vx::CEN_APPEND, s);
         if (e != cudaSuccess) return cuda_fail(e, "centroid append launch");
     }
     // the scorer may always launch early: before its dependency wait it reads nothing, or
@@ -715,19 +756,83 @@ vx_status fused_step(const vx_geometry *geo, const vx_page_table *table, const v
     e = vx::launch_topk(topk_args(geo, table, scores, k, seed, sel, err), mode, s, true);
     if (e != cudaSuccess) return cuda_fail(e, "top-k launch");
     return do_decode(geo, table, q, k_cache, v_cache, sel, k, sm_scale, p, l, ws, out, lse, err, s, true,
-                     p.chunks > p.static_chunks ? dctr : nullptr);
+                     p.chunks > p.static_chunks ? dctr : nullptr, quant);
 }
 
 }  // namespace
 
 extern "C" {
 
+vx_status vx_sparse_decode(const vx_geometry *geo, const vx_page_table *table, const void *q, const void *k_cache,
+                           const void *v_cache, const int32_t *sel, int32_t k, float sm_scale, int32_t num_splits,
+                           void *out, float *lse, void *ws, size_t ws_bytes, int32_t *err, void *stream) {
+    VX_TRY(check_geo(geo, table));
+    VX_TRY(check_ptr(q, "q"));
+    VX_TRY(check_ptr(k_cache, "k_cache"));
+    if (!geo->mla_shared_kv) VX_TRY(check_ptr(v_cache, "v_cache"));
+    return sparse_decode(geo, table, q, k_cache, v_cache, nullptr, sel, k, sm_scale, num_splits, out, lse, ws, ws_bytes,
+                         err, stream);
+}
+
+vx_status vx_sparse_decode_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
+                                 const vx_quant_cache *cache, const int32_t *sel, int32_t k, float sm_scale,
+                                 int32_t num_splits, void *out, float *lse, void *ws, size_t ws_bytes, int32_t *err,
+                                 void *stream) {
+    VX_TRY(check_geo(geo, table));
+    VX_TRY(check_ptr(q, "q"));
+    VX_TRY(check_quant(geo, cache));
+    return sparse_decode(geo, table, q, nullptr, nullptr, cache, sel, k, sm_scale, num_splits, out, lse, ws, ws_bytes,
+                         err, stream);
+}
+
+vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, const vx_quant_cache *cache,
+                          void *centroids, const void *k_new, const void *v_new, const int32_t *first_pos,
+                          int32_t *err, void *stream) {
+    VX_TRY(check_geo(geo, table));
+    VX_TRY(check_quant(geo, cache));
+    VX_TRY(check_ptr(centroids, "centroids"));
+    VX_TRY(check_ptr(k_new, "k_new"));
+    VX_TRY(check_ptr(v_new, "v_new"));
+    if (first_pos && !al4(first_pos)) return fail(VX_ERR_INVALID_ARG, "first_pos must be 4-byte aligned");
+    if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
+    cudaError_t e = vx::launch_quant_update(
+        centroid_args(geo, table, nullptr, nullptr, centroids, k_new, v_new, first_pos, err), quant_args(cache),
+        first_pos ? vx::CEN_PREFILL : vx::CEN_APPEND, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "quantising write launch");
+    return VX_OK;
+}
+
+vx_status vx_block_topk_decode_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
+                                     const vx_quant_cache *cache, const void *centroids, int32_t k, int32_t mode,
+                                     uint64_t seed, float sm_scale, int32_t score_dims, int32_t num_splits, void *out,
+                                     float *lse, float *scores_out, int32_t *sel_out, void *ws, size_t ws_bytes,
+                                     int32_t *err, void *stream) {
+    if (!cache) return fail(VX_ERR_INVALID_ARG, "quantised cache is NULL");
+    return fused_step(geo, table, q, nullptr, nullptr, cache, centroids, nullptr, nullptr, nullptr, nullptr, nullptr, k,
+                      mode, seed, sm_scale, score_dims, num_splits, out, lse, scores_out, sel_out, ws, ws_bytes, err,
+                      stream);
+}
+
+vx_status vx_block_topk_decode_append_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
+                                            const vx_quant_cache *cache, void *centroids, const void *k_new,
+                                            const void *v_new, int32_t k, int32_t mode, uint64_t seed, float sm_scale,
+                                            int32_t score_dims, int32_t num_splits, void *out, float *lse,
+                                            float *scores_out, int32_t *sel_out, void *ws, size_t ws_bytes,
+                                            int32_t *err, void *stream) {
+    if (!cache) return fail(VX_ERR_INVALID_ARG, "quantised cache is NULL");
+    if (!k_new)
+        return fail(VX_ERR_INVALID_ARG, "k_new is NULL (use vx_block_topk_decode_quant for a step without append)");
+    return fused_step(geo, table, q, nullptr, nullptr, cache, centroids, nullptr, nullptr, centroids, k_new, v_new, k,
+                      mode, seed, sm_scale, score_dims, num_splits, out, lse, scores_out, sel_out, ws, ws_bytes, err,
+                      stream);
+}
+
 vx_status vx_block_topk_decode(const vx_geometry *geo, const vx_page_table *table, const void *q, const void *k_cache,
                                const void *v_cache, const void *centroids, int32_t k, int32_t mode, uint64_t seed,
                                float sm_scale, int32_t score_dims, int32_t num_splits, void *out, float *lse,
                                float *scores_out, int32_t *sel_out, void *ws, size_t ws_bytes, int32_t *err,
                                void *stream) {
-    return fused_step(geo, table, q, k_cache, v_cache, centroids, nullptr, nullptr, nullptr, nullptr, nullptr, k, mode,
+    return fused_step(geo, table, q, k_cache, v_cache, nullptr, centroids, nullptr, nullptr, nullptr, nullptr, nullptr, k, mode,
                       seed, sm_scale, score_dims, num_splits, out, lse, scores_out, sel_out, ws, ws_bytes, err,
                       stream);
 }
@@ -738,7 +843,7 @@ vx_status vx_block_topk_decode_append(const vx_geometry *geo, const vx_page_tabl
                                       int32_t score_dims, int32_t num_splits, void *out, float *lse, float *scores_out,
                                       int32_t *sel_out, void *ws, size_t ws_bytes, int32_t *err, void *stream) {
     if (!k_new) return fail(VX_ERR_INVALID_ARG, "k_new is NULL (use vx_block_topk_decode for a step without append)");
-    return fused_step(geo, table, q, k_cache, v_cache, centroids, k_cache, v_cache, centroids, k_new, v_new, k, mode,
+    return fused_step(geo, table, q, k_cache, v_cache, nullptr, centroids, k_cache, v_cache, centroids, k_new, v_new, k, mode,
                       seed, sm_scale, score_dims, num_splits, out, lse, scores_out, sel_out, ws, ws_bytes, err,
                       stream);
 }

@@ -211,6 +211,31 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4 &v, float (&f)[8]) {
     }
 }
 
+// Round a double to the nearest bf16, ties to even, directly from the double.
+__device__ __forceinline__ uint16_t f64_to_bf16_rne(double x) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
+    const uint16_t sign = static_cast<uint16_t>((u >> 48) & 0x8000u);
+    const int ebits = static_cast<int>((u >> 52) & 0x7ff);
+    if (ebits == 0x7ff) return (u & 0xfffffffffffffull) ? uint16_t(0x7fc0) : uint16_t(sign | 0x7f80);
+    const double ax = fabs(x);
+    if (ax == 0.0) return sign;
+    const int e = ebits - 1023;  // ax in [2^e, 2^(e+1)) for normal doubles (ours always are)
+    if (e < -126) {
+        // bf16 subnormal range: spacing 2^-133
+        const long long q = __double2ll_rn(ax * 0x1p133);  // exact scaling, RNE to integer
+        return static_cast<uint16_t>(sign | static_cast<uint16_t>(q));  // q == 128 -> min normal
+    }
+    // 8 significant bits: scale into [128, 256) and round to an integer, ties to even
+    long long q = __double2ll_rn(scalbn(ax, 7 - e));
+    int ee = e;
+    if (q == 256) {
+        q = 128;
+        ++ee;
+    }
+    if (ee > 127) return static_cast<uint16_t>(sign | 0x7f80);
+    return static_cast<uint16_t>(sign | ((ee + 127) << 7) | (static_cast<int>(q) & 0x7f));
+}
+
 __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
 
 }  // namespace vx

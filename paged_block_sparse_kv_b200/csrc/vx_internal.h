@@ -93,6 +93,49 @@ struct DecodeArgs {
     float scale_log2;         // sm_scale * log2(e)
 };
 
+// 8-bit cache: the decode reads it besides DecodeArgs, the quantising write besides CentroidArgs
+struct QuantArgs {
+    uint8_t *k_cache, *v_cache;  // codes
+    float *k_scale, *v_scale;    // [num_pool_pages][Hkv]
+    int32_t format;              // VX_QUANT_INT8 or VX_QUANT_E4M3
+};
+
+// The arrays of a page pool: bytes of one page of each (zero: the array is absent)
+struct PoolArrays {
+    uint8_t *k, *v, *cen;
+    float *ks, *vs;
+};
+struct PageArgs {
+    PoolArrays src, dst;
+    int32_t kb, vb, cb;      // bytes of a page's keys, values, centroids (multiples of 16)
+    int32_t Hkv, P;
+    int64_t src_pages, num_pages;
+    const int32_t *page_ptr, *page_indices, *seq_lens;
+    int32_t B, max_pages;
+    const int32_t *ref_in;
+    int32_t *ref_out;
+    int32_t *err;
+    // copy
+    const int32_t *copy_src, *copy_dst;
+    int32_t num_copies, one_pool;
+    // update
+    const int32_t *parent, *grow, *new_ptr;
+    int32_t *new_indices, *new_lens;
+    int32_t new_rows, new_max_pages;
+    int64_t num_indices;
+    // compact
+    int32_t *indices_out, *remap, *num_live;
+    // workspace: head words, then arrays (see k_pages.cu)
+    int32_t *head, *list_a, *list_b, *list_c;
+};
+
+// New tokens request i writes in a prefill: seq_lens[i] - first_pos[i], or none for a request
+// whose length or first position is out of range (reported by its own blocks).
+__device__ __forceinline__ int64_t prefill_count(const CentroidArgs &a, int i) {
+    const int32_t L = a.seq_lens[i], fp = a.first_pos[i];
+    return (L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L) ? (int64_t)(L - fp) : 0;
+}
+
 // One decode work unit (a 16-token tile of a selected page) after its metadata has been
 // looked up: row, tensor-map page(-head) index, token offset in the page, valid tokens.
 struct Resolved {
@@ -145,6 +188,14 @@ cudaError_t launch_decode_gqa(const DecodeArgs &a, const CUtensorMap &tmK, const
 // grid = split count (one CTA per split); tmQ views q as (64 columns, rows = batch * Hq, 9 blocks)
 cudaError_t launch_decode_mla(const DecodeArgs &a, const CUtensorMap &tmK, const CUtensorMap &tmQ, int grid,
                               cudaStream_t s, bool pdl);
+// grid: blocks of DEC_WARPS warps; tmK and tmV view the codes as (head_dim, page_size, page-heads)
+cudaError_t launch_decode_quant(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK,
+                                const CUtensorMap &tmV, int grid, cudaStream_t s, bool pdl);
+// a.k_cache, a.v_cache unused; mode CEN_APPEND or CEN_PREFILL
+cudaError_t launch_quant_update(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s);
+cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s);
+cudaError_t launch_update_table(const PageArgs &a, cudaStream_t s);
+cudaError_t launch_compact_pages(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_merge(const DecodeArgs &a, cudaStream_t s, bool pdl);
 // grid = SM count (one block of FUSED_WARPS warps per SM)
 cudaError_t launch_fused(const FusedArgs &a, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t s);
@@ -155,6 +206,12 @@ size_t fused_smem_bytes(int32_t B);
 // Bytes of split partials vx_sparse_decode needs for this problem (validates the geometry).
 vx_status decode_partial_bytes(const vx_geometry *geo, int32_t max_pages, int32_t k, int32_t num_splits,
                                size_t *bytes);
+// Validation shared with the page calls: geometry, page table and pointers (name for the message).
+vx_status validate_geometry(const vx_geometry *geo);
+vx_status validate_table(const vx_geometry *geo, const vx_page_table *table);
+vx_status validate_ptr(const void *p, const char *name, bool can_be_null);
+// SMs of the current device (0: the query failed)
+int current_sm_count();
 // Set the message vx_last_error() returns on this host thread; returns s.
 vx_status set_error(vx_status s, const char *msg);
 // Bytes of split partials of the sparse decode with the partials packed alone (outputs
