@@ -1,4 +1,5 @@
-"""Build libvx.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build libvx.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and _vx_marshal (argument marshalling of
+the 8-bit cache and page calls for Python, C++ against torch's headers) beside it.
 
     python -m paged_block_sparse_kv_b200.build [--force] [--verbose]
 
@@ -15,6 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libvx.so")
+MARSHAL = os.path.join(HERE, "_vx_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -35,7 +38,28 @@ def _stale():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    header = os.path.join(ROOT, "include", "vx.h")
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(MARSHAL) >= os.path.getmtime(p)
+                                                     for p in (MARSHAL_SRC, header)):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = MARSHAL + ".tmp"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, MARSHAL_SRC,
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+                    "-isystem", os.path.join(cuda, "include"), "-L" + os.path.join(base, "lib"),
+                    "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_marshal(force)
     if not force and not _stale():
         return LIB
     objdir = os.path.join(ROOT, "_build", "libvx")

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_update(const CentroidAr
         for (int w = 0; w < QZ_WARPS; ++w) row0 += s_part[w];
         fp = a.first_pos[b];
     }
-    if (L < 1 || L > a.max_pages * a.P || fp < 0 || fp > L) {
+    if (L < 1 || L > a.max_pages * a.P || fp < 0 || fp > L || (!APPEND && row0 + (L - fp) > qa.num_new)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
         return;
     }

@@ -360,7 +360,7 @@ vx_status check_quant(const vx_geometry *g, const vx_quant_cache *c) {
 }
 
 vx::QuantArgs quant_args(const vx_quant_cache *c) {
-    return {static_cast<uint8_t *>(c->k_cache), static_cast<uint8_t *>(c->v_cache), c->k_scale, c->v_scale, c->format};
+    return {static_cast<uint8_t *>(c->k_cache), static_cast<uint8_t *>(c->v_cache), c->k_scale, c->v_scale, c->format, 0};
 }
 
 // ------------------------------------------------------------------ shared launch pieces
@@ -786,8 +786,8 @@ vx_status vx_sparse_decode_quant(const vx_geometry *geo, const vx_page_table *ta
 }
 
 vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, const vx_quant_cache *cache,
-                          void *centroids, const void *k_new, const void *v_new, const int32_t *first_pos,
-                          int32_t *err, void *stream) {
+                          void *centroids, const void *k_new, const void *v_new, int64_t num_new,
+                          const int32_t *first_pos, int32_t *err, void *stream) {
     VX_TRY(check_geo(geo, table));
     VX_TRY(check_quant(geo, cache));
     VX_TRY(check_ptr(centroids, "centroids"));
@@ -795,8 +795,12 @@ vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, co
     VX_TRY(check_ptr(v_new, "v_new"));
     if (first_pos && !al4(first_pos)) return fail(VX_ERR_INVALID_ARG, "first_pos must be 4-byte aligned");
     if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
+    if (num_new < 0 || (!first_pos && num_new < geo->batch))
+        return fail(VX_ERR_INVALID_ARG, "num_new %lld rows: an append needs one per request", (long long)num_new);
+    vx::QuantArgs qa = quant_args(cache);
+    qa.num_new = num_new;
     cudaError_t e = vx::launch_quant_update(
-        centroid_args(geo, table, nullptr, nullptr, centroids, k_new, v_new, first_pos, err), quant_args(cache),
+        centroid_args(geo, table, nullptr, nullptr, centroids, k_new, v_new, first_pos, err), qa,
         first_pos ? vx::CEN_PREFILL : vx::CEN_APPEND, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "quantising write launch");
     return VX_OK;

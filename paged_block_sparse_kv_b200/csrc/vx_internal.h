@@ -98,6 +98,7 @@ struct QuantArgs {
     uint8_t *k_cache, *v_cache;  // codes
     float *k_scale, *v_scale;    // [num_pool_pages][Hkv]
     int32_t format;              // VX_QUANT_INT8 or VX_QUANT_E4M3
+    int64_t num_new;             // prefill write: rows of k_new and v_new
 };
 
 // The arrays of a page pool: bytes of one page of each (zero: the array is absent)

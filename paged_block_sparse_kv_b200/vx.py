@@ -1,4 +1,5 @@
-"""Python binding of libvx (include/vx.h): argument marshalling only.
+"""Python binding of libvx (include/vx.h): argument marshalling only (ctypes, and _vx_marshal for the 8-bit cache and
+page calls).
 
 Every function has the name of the C entry point it calls and does nothing but turn
 torch tensors into pointers and sizes, call the library on the current CUDA stream and
@@ -85,7 +86,7 @@ def lib():
         L.vx_block_topk_decode_append.argtypes = [G, T, p, p, p, p, p, p, i32, i32, u64, f32, i32, i32, p, p, p, p,
                                                   p, sz, p, p]
         Q, O = ctypes.POINTER(vx_quant_cache), ctypes.POINTER(vx_page_pool)
-        L.vx_quant_update.argtypes = [G, T, Q, p, p, p, p, p, p]
+        L.vx_quant_update.argtypes = [G, T, Q, p, p, p, i64, p, p, p]
         L.vx_sparse_decode_quant.argtypes = [G, T, p, Q, p, i32, f32, i32, p, p, p, sz, p, p]
         L.vx_block_topk_decode_quant.argtypes = [G, T, p, Q, p, i32, i32, u64, f32, i32, i32, p, p, p, p, p, sz, p, p]
         L.vx_block_topk_decode_append_quant.argtypes = [G, T, p, Q, p, p, p, i32, i32, u64, f32, i32, i32, p, p, p, p,
@@ -272,9 +273,28 @@ def vx_block_topk_decode_persistent(geo: Geometry, table: PageTable, q, k_cache,
 # ---------------------------------------------------------------------- 8-bit caches and pages
 #
 # These calls also check shapes and devices, and run on the device their tensors lie on (the
-# stream given, or that device's current one), whatever the current device is.
+# stream given, or that device's current one), whatever the current device is.  The checks and
+# the C call are in _vx_marshal (csrc/marshal.cpp): from Python they would take longer than the
+# kernels.
 
-_CODES = {torch.int8: VX_QUANT_INT8, torch.float8_e4m3fn: VX_QUANT_E4M3}
+_native = None
+
+
+def _marshal():
+    """The loaded _vx_marshal, bound to libvx.so's entry points (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        L = lib()
+        from . import _vx_marshal as m
+        m.bind(*[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in
+                 ("vx_quant_update", "vx_sparse_decode_quant", "vx_block_topk_decode_quant",
+                  "vx_block_topk_decode_append_quant", "vx_copy_pages", "vx_update_table", "vx_compact_pages")])
+        _native = m
+    return _native
+
+
+def _on(stream):
+    return None if stream is None else (stream.cuda_stream, stream.device.index)
 
 
 @dataclass
@@ -284,19 +304,6 @@ class QuantCache:
     v_cache: torch.Tensor  # the same type and shape
     k_scale: torch.Tensor  # float32 [Npool][Hkv]
     v_scale: torch.Tensor  # float32 [Npool][Hkv]
-
-    def c(self, geo: Geometry) -> vx_quant_cache:
-        if self.k_cache.dtype not in _CODES:
-            raise TypeError(f"k_cache must be int8 or float8_e4m3fn, got {self.k_cache.dtype}")
-        codes = (geo.num_pool_pages, geo.num_kv_heads, geo.page_size, geo.head_dim_qk)
-        scales = codes[:2]
-        return vx_quant_cache(_CODES[self.k_cache.dtype], _shaped(self.k_cache, "k_cache", codes, self.k_cache.dtype),
-                              _shaped(self.v_cache, "v_cache", codes, self.k_cache.dtype),
-                              _shaped(self.k_scale, "k_scale", scales, torch.float32),
-                              _shaped(self.v_scale, "v_scale", scales, torch.float32))
-
-    def tensors(self):
-        return [self.k_cache, self.v_cache, self.k_scale, self.v_scale]
 
 
 @dataclass
@@ -308,107 +315,28 @@ class PagePool:
     k_scale: Optional[torch.Tensor] = None      # float32 [Npool][Hkv], 8-bit pools only
     v_scale: Optional[torch.Tensor] = None
 
-    def c(self, geo: Geometry) -> vx_page_pool:
-        dtype = self.k_cache.dtype
-        if dtype != torch.bfloat16 and dtype not in _CODES:
-            raise TypeError(f"k_cache must be bfloat16, int8 or float8_e4m3fn, got {dtype}")
-        n, h = self.k_cache.shape[0], geo.num_kv_heads
-        return vx_page_pool(_shaped(self.k_cache, "k_cache", (n, h, geo.page_size, geo.head_dim_qk), dtype),
-                            _shaped(self.v_cache, "v_cache", (n, h, geo.page_size, geo.head_dim_v), dtype),
-                            _shaped(self.centroids, "centroids", (n, h, geo.head_dim_qk), torch.bfloat16),
-                            _shaped(self.k_scale, "k_scale", (n, h), torch.float32),
-                            _shaped(self.v_scale, "v_scale", (n, h), torch.float32),
-                            1 if dtype in _CODES else 2, n)
-
-    def tensors(self):
-        return [t for t in (self.k_cache, self.v_cache, self.centroids, self.k_scale, self.v_scale) if t is not None]
-
-
-def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype):
-    """Pointer of an optional contiguous tensor; None in `shape` stands for any extent."""
-    if t is None:
-        return None
-    _check(t, dtype)
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _table_c(geo: Geometry, table: PageTable) -> vx_page_table:
-    for name in ("page_ptr", "seq_lens"):
-        _shaped(getattr(table, name), name, (geo.batch,), torch.int32)
-    return table.c()
-
-
-def _run(fn, tensors, stream, *args):
-    """Call a C entry point on the device that every tensor lies on."""
-    device = tensors[0].device
-    if device.type != "cuda":
-        raise ValueError("libvx works on CUDA tensors")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and on {t.device} in one call")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"tensors on {device}, stream on {stream.device}")
-    with torch.cuda.device(device):
-        _ok(fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream))
-
-
-def _table_tensors(table: PageTable):
-    return [table.page_ptr, table.page_indices, table.seq_lens]
-
 
 def vx_quant_update(geo: Geometry, table: PageTable, cache: QuantCache, centroids, k_new, v_new, first_pos=None,
                     err=None, stream=None):
     """Quantise one new token per request (k_new, v_new [B][Hkv][D]), or a prefill chunk (k_new,
     v_new [N][Hkv][D] packed in request order, with first_pos), into an 8-bit cache; scales and
     centroids of the pages touched follow.  N is the sum of seq_lens - first_pos."""
-    n, h, d = (None if first_pos is not None else geo.batch), geo.num_kv_heads, geo.head_dim_qk
-    ptrs = [_shaped(centroids, "centroids", (geo.num_pool_pages, h, d), torch.bfloat16),
-            _shaped(k_new, "k_new", (n, h, d), torch.bfloat16), _shaped(v_new, "v_new", (n, h, d), torch.bfloat16),
-            _shaped(first_pos, "first_pos", (geo.batch,), torch.int32), _ptr(err, torch.int32)]
-    _run(lib().vx_quant_update, [k_new, v_new, centroids, first_pos, err] + cache.tensors() + _table_tensors(table),
-         stream, ctypes.byref(geo.c()), ctypes.byref(_table_c(geo, table)), ctypes.byref(cache.c(geo)), *ptrs)
-
-
-def _query_out(geo: Geometry, q, out, lse):
-    rows = (geo.batch, geo.num_q_heads)
-    return (_shaped(q, "q", rows + (geo.head_dim_qk,), torch.bfloat16),
-            _shaped(out, "out", rows + (geo.head_dim_v,), torch.bfloat16), _shaped(lse, "lse", rows, torch.float32))
+    _ok(_marshal().quant_update(geo, table, cache, centroids, k_new, v_new, first_pos, err, _on(stream)))
 
 
 def vx_sparse_decode_quant(geo: Geometry, table: PageTable, q, cache: QuantCache, sel, k: int, out, ws, lse=None,
                            sm_scale=0.0, num_splits=0, err=None, stream=None):
     """vx_sparse_decode over an 8-bit cache."""
-    pq, po, pl = _query_out(geo, q, out, lse)
-    _run(lib().vx_sparse_decode_quant, [q, sel, out, lse, ws, err] + cache.tensors() + _table_tensors(table), stream,
-         ctypes.byref(geo.c()), ctypes.byref(_table_c(geo, table)), pq, ctypes.byref(cache.c(geo)),
-         _shaped(sel, "sel", (geo.batch, geo.num_kv_heads, k), torch.int32), k, float(sm_scale), num_splits, po, pl,
-         _ptr(ws), ws.numel() * ws.element_size(), _ptr(err, torch.int32))
-
-
-def _chained(geo, table, q, cache, centroids, new, k, out, ws, lse, mode, seed, sm_scale, score_dims, num_splits,
-             scores_out, sel_out, err, stream):
-    pq, po, pl = _query_out(geo, q, out, lse)
-    rows = (geo.batch, geo.num_kv_heads)
-    fn = lib().vx_block_topk_decode_append_quant if new else lib().vx_block_topk_decode_quant
-    tensors = [q, centroids, *new, out, lse, scores_out, sel_out, ws, err] + cache.tensors() + _table_tensors(table)
-    _run(fn, tensors, stream, ctypes.byref(geo.c()), ctypes.byref(_table_c(geo, table)), pq,
-         ctypes.byref(cache.c(geo)),
-         _shaped(centroids, "centroids", (geo.num_pool_pages, geo.num_kv_heads, geo.head_dim_qk), torch.bfloat16),
-         *[_shaped(x, name, rows + (geo.head_dim_qk,), torch.bfloat16) for name, x in zip(("k_new", "v_new"), new)],
-         k, mode, seed & (2 ** 64 - 1), float(sm_scale), score_dims, num_splits, po, pl,
-         _shaped(scores_out, "scores_out", rows + (table.max_pages,), torch.float32),
-         _shaped(sel_out, "sel_out", rows + (k,), torch.int32), _ptr(ws), ws.numel() * ws.element_size(),
-         _ptr(err, torch.int32))
+    _ok(_marshal().sparse_decode_quant(geo, table, q, cache, sel, k, out, ws, lse, sm_scale, num_splits, err,
+                                       _on(stream)))
 
 
 def vx_block_topk_decode_quant(geo: Geometry, table: PageTable, q, cache: QuantCache, centroids, k: int, out, ws,
                                lse=None, mode=0, seed=0, sm_scale=0.0, score_dims=0, num_splits=0, scores_out=None,
                                sel_out=None, err=None, stream=None):
     """vx_block_topk_decode over an 8-bit cache: score, select, attend."""
-    _chained(geo, table, q, cache, centroids, (), k, out, ws, lse, mode, seed, sm_scale, score_dims, num_splits,
-             scores_out, sel_out, err, stream)
+    _ok(_marshal().block_topk_decode_quant(geo, table, q, cache, centroids, None, None, k, out, ws, lse, mode, seed,
+                                           sm_scale, score_dims, num_splits, scores_out, sel_out, err, _on(stream)))
 
 
 def vx_block_topk_decode_append_quant(geo: Geometry, table: PageTable, q, cache: QuantCache, centroids, k_new, v_new,
@@ -416,8 +344,9 @@ def vx_block_topk_decode_append_quant(geo: Geometry, table: PageTable, q, cache:
                                       num_splits=0, scores_out=None, sel_out=None, err=None, stream=None):
     """One appending decode step over an 8-bit cache: quantise each request's new token into its
     page, then score, select and attend."""
-    _chained(geo, table, q, cache, centroids, (k_new, v_new), k, out, ws, lse, mode, seed, sm_scale, score_dims,
-             num_splits, scores_out, sel_out, err, stream)
+    _ok(_marshal().block_topk_decode_append_quant(geo, table, q, cache, centroids, k_new, v_new, k, out, ws, lse, mode,
+                                                  seed, sm_scale, score_dims, num_splits, scores_out, sel_out, err,
+                                                  _on(stream)))
 
 
 def vx_page_workspace_size(geo: Geometry, rows: int) -> int:
@@ -429,13 +358,7 @@ def vx_page_workspace_size(geo: Geometry, rows: int) -> int:
 
 def vx_copy_pages(geo: Geometry, src: PagePool, dst: PagePool, src_pages, dst_pages, ws, err=None, stream=None):
     """Page src_pages[i] of `src` to page dst_pages[i] of `dst` (which may be the same pool)."""
-    n = src_pages.numel()
-    if src.k_cache.dtype != dst.k_cache.dtype:
-        raise TypeError("the pools must hold the same type")
-    _run(lib().vx_copy_pages, [src_pages, dst_pages, ws, err] + src.tensors() + dst.tensors(), stream,
-         ctypes.byref(geo.c()), ctypes.byref(src.c(geo)), ctypes.byref(dst.c(geo)),
-         _shaped(src_pages, "src_pages", (n,), torch.int32), _shaped(dst_pages, "dst_pages", (n,), torch.int32), n,
-         _ptr(ws), ws.numel() * ws.element_size(), _ptr(err, torch.int32))
+    _ok(_marshal().copy_pages(geo, src, dst, src_pages, dst_pages, ws, err, _on(stream)))
 
 
 def vx_update_table(geo: Geometry, pool: PagePool, table: PageTable, ref, parent, grow, new_table: PageTable, new_ref,
@@ -443,28 +366,11 @@ def vx_update_table(geo: Geometry, pool: PagePool, table: PageTable, ref, parent
     """New rows of a page table: row i takes over the tokens of row parent[i] (-1: none) and gets
     room for grow[i] more; new_table.page_ptr is an input, its page_indices and seq_lens and
     new_ref (which may be ref) are written."""
-    rows, pages = parent.numel(), (geo.num_pool_pages,)
-    _run(lib().vx_update_table,
-         [ref, new_ref, parent, grow, ws, err] + pool.tensors() + _table_tensors(table) + _table_tensors(new_table),
-         stream, ctypes.byref(geo.c()), ctypes.byref(pool.c(geo)), ctypes.byref(_table_c(geo, table)),
-         _shaped(ref, "ref", pages, torch.int32), _shaped(parent, "parent", (rows,), torch.int32),
-         _shaped(grow, "grow", (rows,), torch.int32), rows,
-         _shaped(new_table.page_ptr, "new page_ptr", (rows,), torch.int32), _ptr(new_table.page_indices, torch.int32),
-         new_table.page_indices.numel(), _shaped(new_table.seq_lens, "new seq_lens", (rows,), torch.int32),
-         new_table.max_pages, _shaped(new_ref, "new_ref", pages, torch.int32), _ptr(ws),
-         ws.numel() * ws.element_size(), _ptr(err, torch.int32))
+    _ok(_marshal().update_table(geo, pool, table, ref, parent, grow, new_table, new_ref, ws, err, _on(stream)))
 
 
 def vx_compact_pages(geo: Geometry, pool: PagePool, table: PageTable, ref, new_indices, new_ref, remap, num_live, ws,
                      err=None, stream=None):
     """Move every live page (ref > 0) into the lowest ids; new_indices and new_ref may be
     table.page_indices and ref."""
-    pages = (geo.num_pool_pages,)
-    _run(lib().vx_compact_pages,
-         [ref, new_indices, new_ref, remap, num_live, ws, err] + pool.tensors() + _table_tensors(table), stream,
-         ctypes.byref(geo.c()), ctypes.byref(pool.c(geo)), ctypes.byref(_table_c(geo, table)),
-         _shaped(ref, "ref", pages, torch.int32),
-         _shaped(new_indices, "new_indices", tuple(table.page_indices.shape), torch.int32),
-         _shaped(new_ref, "new_ref", pages, torch.int32), _shaped(remap, "remap", pages, torch.int32),
-         _shaped(num_live, "num_live", (1,), torch.int32), _ptr(ws), ws.numel() * ws.element_size(),
-         _ptr(err, torch.int32))
+    _ok(_marshal().compact_pages(geo, pool, table, ref, new_indices, new_ref, remap, num_live, ws, err, _on(stream)))

@@ -375,6 +375,19 @@ def test_write_bad_rows_are_reported_and_skipped():
     check_cache(c, cache, cen, want)
 
 
+def test_prefill_rows_past_the_input_are_refused():
+    """Fewer new rows than the table says: the requests that would read past them write nothing."""
+    c = Case("int8", [20, 30, 5], 2, 2, 64, 16, seed=1).blank()
+    cache, cen = c.cache(), torch.zeros(c.pool, 2, 64, dtype=torch.bfloat16, device=DEV)
+    want = np.zeros((c.pool, 2, 64))
+    x = new_rows(c, 49)
+    vx.vx_quant_update(c.geo, c.table, cache, cen, x.to(DEV), x.to(DEV), first_pos=dev(np.zeros(3)), err=c.err)
+    assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN
+    for a, s, w in ((c.k, c.ks, want), (c.v, c.vs, None)):
+        ref.quant_update(a, s, w, x.double().numpy(), c.ptr, c.idx, [20], [0], "int8")
+    check_cache(c, cache, cen, want)
+
+
 # ------------------------------------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("fmt", FMTS)

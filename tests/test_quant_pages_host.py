@@ -55,7 +55,7 @@ CACHES = [dict(format=0), dict(format=3), dict(k_cache=None), dict(v_cache=FAKE 
 @pytest.mark.parametrize("kw", CACHES)
 def test_bad_caches(L, kw):
     c = _cache(**kw)
-    assert L.vx_quant_update(_geo(), _table(), c, FAKE, FAKE, FAKE, None, None, None) == INVALID
+    assert L.vx_quant_update(_geo(), _table(), c, FAKE, FAKE, FAKE, 2, None, None, None) == INVALID
     assert L.vx_sparse_decode_quant(_geo(), _table(), FAKE, c, FAKE, 4, F0, 8, FAKE, None, FAKE, 1 << 30, None,
                                     None) == INVALID
     assert L.vx_block_topk_decode_quant(_geo(), _table(), FAKE, c, FAKE, 4, 0, 0, F0, 0, 8, FAKE, None, None, None, FAKE,
@@ -67,13 +67,13 @@ def test_bad_caches(L, kw):
 
 def test_quant_calls_refuse(L):
     c = _cache()
-    up = lambda g=None, t=None, cache=c, cen=FAKE, k=FAKE, v=FAKE, first=None, err=None: L.vx_quant_update(
-        g or _geo(), t or _table(), cache, cen, k, v, first, err, None)
+    up = lambda g=None, t=None, cache=c, cen=FAKE, k=FAKE, v=FAKE, n=2, first=None, err=None: \
+        L.vx_quant_update(g or _geo(), t or _table(), cache, cen, k, v, n, first, err, None)
     assert up(g=_geo(**MLA)) == UNSUPPORTED
     assert up(g=_geo(head_dim_qk=96, head_dim_v=96)) == UNSUPPORTED
     assert up(t=_table(max_pages=0)) == INVALID
     for kw in (dict(cache=None), dict(cen=None), dict(k=None), dict(v=None), dict(k=FAKE + 8), dict(first=FAKE + 2),
-               dict(err=FAKE + 1)):
+               dict(err=FAKE + 1), dict(n=1), dict(n=-1, first=FAKE)):
         assert up(**kw) == INVALID
     dec = lambda g=None, cache=c, q=FAKE, sel=FAKE, k=4, scale=0.0, out=FAKE, lse=None, ws=FAKE, n=1 << 30, err=None: \
         L.vx_sparse_decode_quant(g or _geo(), _table(), q, cache, sel, k, ctypes.c_float(scale), 8, out, lse, ws, n, err,
