@@ -434,8 +434,9 @@ vx_status vx_copy_pages(const vx_geometry *geo, const vx_page_pool *src, const v
  *       written.
  *   new_page_indices, new_seq_lens: outputs, in memory of their own (not the old table's).
  *   new_max_pages: bound on the pages of a new row, as vx_page_table.max_pages.
- * All or nothing: when an old length, a parent, a growth, a new row's place or a forked last
- * page's id is out of range, or the free pages do not suffice, the call sets the bit
+ * All or nothing: when an old length, a parent, a growth or a new row's place is out of range, a
+ * parent's partly filled last page is outside the pool or free, or the free pages do not
+ * suffice, the call sets the bit
  * (VX_DATA_BAD_SEQ_LEN, _BAD_ROW, _BAD_PAGE_ID, _NO_PAGES), every new length to 0 and ref_out
  * to ref_in, and touches neither the pool nor new_page_indices: the old rows are still good.
  * Another old page id outside the pool sets VX_DATA_BAD_PAGE_ID; it is passed on to the new

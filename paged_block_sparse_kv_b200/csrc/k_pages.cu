@@ -1,12 +1,14 @@
 // k_pages.cu -- pages of a pool: copy, new table rows (fork, free, grow), compaction.
 //
-// Each call is a planning kernel and an applying kernel.  The planner is one thread-block
-// cluster: its CTAs split the pool's reference counts, exchange their totals through
-// distributed shared memory and give every free (or live) page its rank by prefix sums, so
-// that the pages handed out depend on the counts alone, never on timing.  The applier fills
-// the GPU: page data moves in pieces of PG_PIECE 16-byte chunks, table rows and reference
-// counts in spans of PG_SPAN entries.  Bound: HBM for the page data (read and written once),
-// latency of a few dependent loads for the planner.
+// The first kernel of an update or a compaction reads the pool's reference counts once, over the
+// whole GPU: a bit per page (free, or live) and the count of each segment of PG_SEG pages.  A
+// block of the next kernel takes the segments' prefix sums into shared memory, so a warp that
+// looks at a segment's 32 words of bits knows the rank of each of its pages: what is handed out
+// or moved depends on the counts alone, never on timing, and no single block has to scan the
+// pool (a cluster of 8 blocks that did took 23 us over 290,000 pages).  Every block has one small
+// job: these kernels run a few microseconds, and instructions are fetched cold.
+// Page data moves in pieces of PG_PIECE 16-byte chunks.  Bound: HBM for page data (read and
+// written once), a few dependent loads for the rest.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -19,97 +21,140 @@ namespace vx {
 
 namespace {
 
-constexpr int PG_CTAS = 8;        // CTAs of the planning cluster
-constexpr int PG_THREADS = 1024;  // threads of a planning CTA
-constexpr int PG_WARPS = PG_THREADS / 32;
+constexpr int PG_CTAS = 8;       // CTAs of the copy planner's cluster
+constexpr int PG_THREADS = 1024; // threads of a planning block
+constexpr int PG_SEG = 1024;     // pages of a segment: 32 words of bits, one 128-byte line
+constexpr int PG_GROUPS = 1024;  // prefix sums a block keeps (a segment each in pools of 2^20 pages)
 constexpr int PG_MAX_ROWS = 4096;
-constexpr int PG_PIECE = 1024;    // 16-byte chunks of a page moved by one block at a time
-constexpr int PG_SPAN = 1024;     // table entries handled by one block at a time
-constexpr int PG_BLOCK = 256;     // threads of an applying block
+constexpr int PG_PIECE = 1024;   // 16-byte chunks of a page moved by one block at a time
+constexpr int PG_SPAN = 256;     // table entries handled by one warp, 8 per lane
+constexpr int PG_BLOCK = 256;    // threads of an applying block
 
-// ------------------------------------------------------------------ ranks over the pool
+// ------------------------------------------------------------------ flags and ranks
 
-// Warp w of the cluster (of PG_CTAS * PG_WARPS) owns pages [w * span, (w + 1) * span), span a
-// multiple of 128: 32 lanes x 4 consecutive pages per step.
-__device__ __forceinline__ int64_t warp_span(int64_t n) {
-    const int64_t w = PG_CTAS * PG_WARPS;
-    return ((n + w - 1) / w + 127) / 128 * 128;
-}
-
-__device__ __forceinline__ int4 load4(const int32_t *p, int64_t at, int64_t n, int fill) {
-    if (at + 4 <= n) return *reinterpret_cast<const int4 *>(p + at);
-    int4 v = make_int4(fill, fill, fill, fill);
-    if (at < n) v.x = p[at];
-    if (at + 1 < n) v.y = p[at + 1];
-    if (at + 2 < n) v.z = p[at + 2];
-    return v;
-}
-
-// Flags of a lane's 4 pages (bit e: page at + e has ref > 0 when LIVE, == 0 otherwise; none past n)
+// Flags of a planning block's 4 * PG_THREADS pages from p0: ref > 0 when LIVE, ref == 0 otherwise,
+// none past the pool; list_a[p / 32] holds the bits, list_b[p / PG_SEG] the segments' counts.  With
+// `out` the reference counts are copied there.
 template <bool LIVE>
-__device__ __forceinline__ uint32_t flags4(const int4 &v, int64_t at, int64_t n) {
+__device__ __forceinline__ void flag_pages(const PageArgs &a, int64_t p0, int32_t *out) {
+    __shared__ int32_t s_count[PG_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t at = p0 + (int64_t)tid * 4, n = a.num_pages;
+    int4 v = make_int4(-1, -1, -1, -1);
+    if (at + 4 <= n) {
+        v = *reinterpret_cast<const int4 *>(a.ref_in + at);
+        if (out) *reinterpret_cast<int4 *>(out + at) = v;
+    } else {
+        int32_t *w[3] = {&v.x, &v.y, &v.z};
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (at + e < n) {
+                *w[e] = a.ref_in[at + e];
+                if (out) out[at + e] = *w[e];
+            }
+    }
     const int r[4] = {v.x, v.y, v.z, v.w};
     uint32_t f = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (at + e < n && (LIVE ? r[e] > 0 : r[e] == 0)) f |= 1u << e;
-    return f;
-}
-
-// Exclusive rank of the calling lane's first flag among the warp's (lane-major order), and the
-// warp's total.
-__device__ __forceinline__ int lane_rank(uint32_t f, int lane, int &total) {
-    int before = 0;
-    total = 0;
+    for (int e = 0; e < 4; ++e) f |= (LIVE ? r[e] > 0 : r[e] == 0) ? 1u << e : 0u;
+    const int count = __reduce_add_sync(FULL, __popc(f));
+    f <<= 4 * (lane & 7);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t b = __ballot_sync(FULL, (f >> e) & 1u);
-        before += __popc(b & ((1u << lane) - 1u));
-        total += __popc(b);
+    for (int off = 1; off < 8; off <<= 1) f |= __shfl_xor_sync(FULL, f, off);
+    if ((lane & 7) == 0 && at < (n + PG_SEG - 1) / PG_SEG * PG_SEG) a.list_a[at / 32] = (int32_t)f;
+    if (lane == 0) s_count[tid >> 5] = count;
+    __syncthreads();
+    constexpr int PER = PG_SEG / 128;  // warps of a segment
+    if (tid < PG_THREADS / 32 / PER && p0 + (int64_t)tid * PG_SEG < n) {
+        int c = 0;
+#pragma unroll
+        for (int w = 0; w < PER; ++w) c += s_count[tid * PER + w];
+        a.list_b[p0 / PG_SEG + tid] = c;
     }
-    return before;
 }
 
-// Count the flagged pages of every warp of the cluster and give each its exclusive base.
-// `s_warp` [PG_WARPS] and `s_total` are shared; each(at, v) sees every lane's loads.
-template <bool LIVE, typename Each>
-__device__ int64_t cluster_base(const int32_t *ref, int64_t n, int32_t *s_warp, int32_t *s_total, int64_t &all,
-                                Each each) {
-    cg::cluster_group cl = cg::this_cluster();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t span = warp_span(n), p0 = ((int64_t)cl.block_rank() * PG_WARPS + warp) * span;
-    int count = 0;
-#pragma unroll 4
-    for (int64_t o = 0; o < span; o += 128) {
-        const int64_t at = p0 + o + lane * 4;
-        const int4 v = load4(ref, at, n, -1);
-        count += __popc(flags4<LIVE>(v, at, n));
-        each(at, v);
-    }
-    count = __reduce_add_sync(FULL, count);
-    if (lane == 0) s_warp[warp] = count;
-    __syncthreads();
-    if (warp == 0) {
-        const int c = s_warp[lane];
-        int x = c;
+// A block's view of the flags: prefix sums of groups of `g` segments in shared memory.
+struct PoolRanks {
+    const int32_t *bits, *counts;
+    const uint32_t *pre;  // [groups + 1], shared
+    int32_t segs, g, groups;
+
+    __device__ __forceinline__ PoolRanks(const PageArgs &a, uint32_t *s_pre, uint32_t *s_warp)
+        : bits(a.list_a), counts(a.list_b), pre(s_pre) {
+        segs = (int)((a.num_pages + PG_SEG - 1) / PG_SEG);
+        g = ceil_div(segs, PG_GROUPS);
+        groups = ceil_div(segs, g);
+        // thread t sums groups [t * per, (t + 1) * per)
+        const int per = ceil_div(groups, PG_BLOCK), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int k0 = min(groups, (int)threadIdx.x * per), k1 = min(groups, k0 + per);
+        uint32_t mine = 0;
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) {
+            s_pre[k] = mine;
+#pragma unroll 1
+            for (int s = k * g; s < min(segs, (k + 1) * g); ++s) mine += (uint32_t)counts[s];
+        }
+        uint32_t x = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(FULL, x, off);
+            const uint32_t y = __shfl_up_sync(FULL, x, off);
             if (lane >= off) x += y;
         }
-        s_warp[lane] = x - c;
-        if (lane == 31) *s_total = x;
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        uint32_t before = x - mine;
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) s_pre[k] += before;
+        if (threadIdx.x == PG_BLOCK - 1) s_pre[groups] = before + mine;
+        __syncthreads();
     }
-    cl.sync();
-    int64_t base = s_warp[warp];
-    all = 0;
-    for (int c = 0; c < PG_CTAS; ++c) {
-        const int t = *cl.map_shared_rank(s_total, c);
-        if (c < (int)cl.block_rank()) base += t;
-        all += t;
+    __device__ __forceinline__ uint32_t total() const { return pre[groups]; }
+    // flagged pages before segment `seg`
+    __device__ __forceinline__ uint32_t before_segment(int seg) const {
+        const int k = seg / g;
+        uint32_t r = pre[k];
+#pragma unroll 1
+        for (int s = k * g; s < seg; ++s) r += (uint32_t)counts[s];
+        return r;
     }
-    return base;
-}
+    // By a whole warp: lane l's word of segment `seg` and the flagged pages before that word
+    __device__ __forceinline__ uint32_t segment_word(int seg, int lane, uint32_t &rank) const {
+        const uint32_t w = (uint32_t)bits[(int64_t)seg * 32 + lane], c = __popc(w);
+        uint32_t x = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t y = __shfl_up_sync(FULL, x, off);
+            if (lane >= off) x += y;
+        }
+        rank = before_segment(seg) + x - c;
+        return w;
+    }
+    // By a whole warp: the flagged page of rank r (below the total)
+    __device__ __forceinline__ uint32_t page_of(uint32_t r, int lane) const {
+        int lo = 0, hi = groups - 1;  // the last group with at most r before it
+#pragma unroll 1
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] <= r) lo = mid;
+            else hi = mid - 1;
+        }
+        int seg = lo * g;
+        if (g > 1) {
+#pragma unroll 1
+            while (before_segment(seg) + (uint32_t)counts[seg] <= r) ++seg;
+        }
+        uint32_t rank;
+        uint32_t w = segment_word(seg, lane, rank);
+        const bool mine = r >= rank && r - rank < (uint32_t)__popc(w);
+        const int src = __ffs(__ballot_sync(FULL, mine)) - 1;
+        w = __shfl_sync(FULL, w, src);
+#pragma unroll 1
+        for (rank = r - __shfl_sync(FULL, rank, src); rank > 0; --rank) w &= w - 1;
+        return (uint32_t)seg * PG_SEG + src * 32 + __ffs(w) - 1;
+    }
+};
 
 // ------------------------------------------------------------------ page data
 
@@ -171,9 +216,9 @@ __global__ void __cluster_dims__(PG_CTAS) __launch_bounds__(PG_THREADS) k_plan_c
 
 __global__ void __launch_bounds__(PG_BLOCK) k_apply_copy(const PageArgs a) {
     pdl_wait();
-    const int pieces = page_pieces(a);
-    for (int64_t it = blockIdx.x; it < (int64_t)a.num_copies * pieces; it += gridDim.x) {
-        const int i = (int)(it / pieces), piece = (int)(it % pieces);
+    const uint32_t pieces = page_pieces(a);
+    for (uint32_t it = blockIdx.x; it < (uint32_t)a.num_copies * pieces; it += gridDim.x) {
+        const int i = it / pieces, piece = it - i * pieces;
         const int32_t s = a.copy_src[i], d = a.copy_dst[i];
         unsigned bad = 0;
         if (s < 0 || s >= a.src_pages || d < 0 || d >= a.num_pages) bad = VX_DATA_BAD_PAGE_ID;
@@ -188,293 +233,326 @@ __global__ void __launch_bounds__(PG_BLOCK) k_apply_copy(const PageArgs a) {
 
 // ------------------------------------------------------------------ new rows
 
-// Shared arrays of the planner, PG_MAX_ROWS ints each
-struct UpdateShared {
-    int32_t *first;  // [old rows] lowest child, INT32_MAX: none
-    int32_t *kids;   // [old rows] children
-    int32_t *off;    // [new rows] rank of the row's first fresh page
-    int32_t *held;   // [new rows] pages taken over from the parent (its last one excluded when copied)
+// Block 0 plans the rows, the others flag the free pages.  What the rows' plan leaves: head[0] the
+// error bits found, head[1] the pages needed (at most 2^31 - 1); list_d[b] 2 * (children of old
+// row b) + (1 when its first child keeps its partly filled last page); for new row i its length
+// and list_c[i]:
+struct RowPlan {
+    int32_t off;   // rank of its first fresh page among the free ones
+    int32_t held;  // entries taken over from the parent
+    int32_t from;  // where they start in page_indices
+    int32_t tail;  // the page that its first fresh page takes a copy of, or -1
 };
-
-// What the applier needs: head[0] 1 (apply) or 0 (refused); list_a[i] the fresh page that takes
-// the copy of new row i's last page, or -1; list_b[b] the change of the references to old row
-// b's whole pages, list_c[b] to its partly filled last page.
-__global__ void __cluster_dims__(PG_CTAS) __launch_bounds__(PG_THREADS) k_plan_update(const PageArgs a) {
-    extern __shared__ int32_t s_rows[];
-    __shared__ int32_t s_warp[PG_WARPS], s_total;
-    __shared__ long long s_scan[PG_WARPS];
-    __shared__ unsigned s_bad;
+__global__ void __launch_bounds__(PG_THREADS) k_plan_update(const PageArgs a) {
     pdl_wait();
     pdl_trigger();
-    cg::cluster_group cl = cg::this_cluster();
+    if (blockIdx.x > 0) {
+        flag_pages<false>(a, (int64_t)(blockIdx.x - 1) * PG_THREADS * 4, a.ref_out != a.ref_in ? a.ref_out : nullptr);
+        return;
+    }
+    __shared__ int32_t s_first[PG_MAX_ROWS];  // [old rows] lowest child, INT32_MAX: none
+    __shared__ int32_t s_kids[PG_MAX_ROWS];   // [old rows] as list_d
+    __shared__ long long s_scan[PG_THREADS / 32];
+    __shared__ unsigned s_bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool lead = cl.block_rank() == 0;
-    const UpdateShared s{s_rows, s_rows + PG_MAX_ROWS, s_rows + 2 * PG_MAX_ROWS, s_rows + 3 * PG_MAX_ROWS};
-    if (tid == 0) s_bad = 0;
-    for (int b = tid; b < a.B; b += PG_THREADS) {
-        s.first[b] = INT32_MAX;
-        s.kids[b] = 0;
-    }
-    __syncthreads();
-    // ---- rows (every CTA does all of them: each needs the offsets)
-    unsigned bad = 0;
-    for (int i = tid; i < a.new_rows; i += PG_THREADS) {
-        const int32_t p = a.parent[i];
-        if (p < -1 || p >= a.B) bad |= VX_DATA_BAD_ROW;
-        else if (p >= 0) {
-            atomicMin(s.first + p, i);
-            atomicAdd(s.kids + p, 1);
+    const int log2_p = __ffs(a.P) - 1;
+    const int per = ceil_div(a.new_rows, PG_THREADS);  // rows [tid * per, (tid + 1) * per) are this thread's
+    const int row0 = tid * per, row1 = min(a.new_rows, row0 + per);
+    struct Row {
+        int32_t p, g, to, L, n, from, tail, tail_ref;
+    };
+    auto load_row = [&](int i) {
+        Row r{a.parent[i], a.grow[i], a.new_ptr[i], 0, 0, 0, -1, 0};
+        if (r.p >= 0 && r.p < a.B) {
+            r.L = a.seq_lens[r.p];
+            if (r.L < 0 || r.L > a.max_pages * a.P) r.L = 0;  // refused below
+            r.from = a.page_ptr[r.p];
+            r.n = (r.L + a.P - 1) >> log2_p;
+            if (r.L & (a.P - 1)) {
+                r.tail = a.page_indices[r.from + r.n - 1];
+                if (r.tail >= 0 && r.tail < a.num_pages) r.tail_ref = a.ref_in[r.tail];
+            }
         }
-    }
+        return r;
+    };
+    Row first_row{};
+    if (row0 < row1) first_row = load_row(row0);
+    if (tid == 0) s_bad = 0;
+    unsigned bad = 0;
     for (int b = tid; b < a.B; b += PG_THREADS) {
+        s_first[b] = INT32_MAX;
+        s_kids[b] = 0;
         const int32_t L = a.seq_lens[b];
         if (L < 0 || L > a.max_pages * a.P) bad |= VX_DATA_BAD_SEQ_LEN;
     }
-    if (bad) atomicOr(&s_bad, bad);
     __syncthreads();
-    const bool sound = s_bad == 0;
-    // rows in order: thread t takes rows [t * per, (t + 1) * per)
-    const int per = ceil_div(a.new_rows, PG_THREADS);
-    long long mine = 0;
-    bad = 0;
-    if (sound) {
-        for (int i = tid * per; i < min(a.new_rows, (tid + 1) * per); ++i) {
-            const int32_t p = a.parent[i], g = a.grow[i];
-            const int32_t L = p >= 0 ? a.seq_lens[p] : 0;
-            const int32_t n = ceil_div(L, a.P);
-            bool copy = false;
-            if (L % a.P) {
-                const int32_t tail = a.page_indices[a.page_ptr[p] + n - 1];
-                if (tail < 0 || tail >= a.num_pages) bad |= VX_DATA_BAD_PAGE_ID;
-                else copy = !(s.first[p] == i && a.ref_in[tail] == 1);
-            }
-            const int64_t L2 = (int64_t)L + g;
-            if (g < 0 || L2 > (int64_t)a.new_max_pages * a.P) {
-                bad |= VX_DATA_BAD_SEQ_LEN;
-                continue;
-            }
-            const int32_t n2 = (int32_t)((L2 + a.P - 1) / a.P);
-            const int32_t to = a.new_ptr[i];
-            if (to < 0 || (int64_t)to + n2 > a.num_indices) bad |= VX_DATA_BAD_ROW;
-            s.off[i] = (n2 - n + (copy ? 1 : 0));
-            s.held[i] = n - (copy ? 1 : 0);
-            mine += s.off[i];
-            if (lead) {
-                a.list_a[i] = -1;
-                if (p >= 0 && s.first[p] == i) a.list_c[p] = copy ? -1 : 0;
-            }
+    for (int i = row0; i < row1; ++i) {
+        const int32_t p = i == row0 ? first_row.p : a.parent[i];
+        if (p < -1 || p >= a.B) bad |= VX_DATA_BAD_ROW;
+        else if (p >= 0) {
+            atomicMin(s_first + p, i);
+            atomicAdd(s_kids + p, 2);
         }
+    }
+    __syncthreads();
+    auto fresh = [&](int i, const Row &r, bool &copy) -> int32_t {  // pages new row i needs
+        copy = r.tail >= 0 && !(s_first[r.p] == i && r.tail_ref == 1);
+        const int64_t L2 = (int64_t)r.L + r.g;
+        if (r.g < 0 || L2 > (int64_t)a.new_max_pages * a.P) {
+            bad |= VX_DATA_BAD_SEQ_LEN;
+            return 0;
+        }
+        const int32_t n2 = (int32_t)((L2 + a.P - 1) >> log2_p);
+        if (r.to < 0 || (int64_t)r.to + n2 > a.num_indices) bad |= VX_DATA_BAD_ROW;
+        // (a last page that is free would be handed out while its row still holds it)
+        if (r.L & (a.P - 1) && r.tail_ref < 1) bad |= VX_DATA_BAD_PAGE_ID;
+        return n2 - r.n + (copy ? 1 : 0);
+    };
+    long long mine = 0;
+    bool first_copy = false;
+    int32_t first_need = 0;
+    for (int i = row0; i < row1; ++i) {
+        const Row r = i == row0 ? first_row : load_row(i);
+        bool copy;
+        const int32_t c = fresh(i, r, copy);
+        if (i == row0) {
+            first_copy = copy;
+            first_need = c;
+        }
+        mine += c;
+        if (r.tail >= 0 && !copy) s_kids[r.p] |= 1;  // the first child alone
     }
     if (bad) atomicOr(&s_bad, bad);
     // exclusive prefix of the rows' fresh pages
-    long long x = mine;
+    auto scan = [&](long long v) {  // inclusive, over a warp
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(FULL, x, off);
-        if (lane >= off) x += y;
-    }
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(FULL, v, off);
+            if (lane >= off) v += y;
+        }
+        return v;
+    };
+    const long long x = scan(mine);
     if (lane == 31) s_scan[warp] = x;
     __syncthreads();
-    long long before = x - mine, need = 0;
-    for (int w = 0; w < PG_WARPS; ++w) {
-        if (w < warp) before += s_scan[w];
-        need += s_scan[w];
+    const long long w = scan(s_scan[lane]);  // every warp for itself: PG_THREADS is 32 warps
+    const long long need = __shfl_sync(FULL, w, 31), warp_before = __shfl_sync(FULL, w, (warp + 31) & 31);
+    long long before = x - mine + (warp > 0 ? warp_before : 0);
+    if (tid == 0) {
+        a.head[0] = (int32_t)s_bad;
+        a.head[1] = (int32_t)min(need, (long long)INT32_MAX);
     }
-    const unsigned rows_bad = s_bad;
-    if (!rows_bad) {
-        for (int i = tid * per; i < min(a.new_rows, (tid + 1) * per); ++i) {
-            const int c = s.off[i];
-            s.off[i] = (int32_t)min(before, (long long)INT32_MAX);
-            before += c;
-        }
+    for (int i = row0; i < row1; ++i) {
+        const Row r = i == row0 ? first_row : load_row(i);
+        bool copy = first_copy;
+        const int32_t c = i == row0 ? first_need : fresh(i, r, copy);
+        reinterpret_cast<RowPlan *>(a.list_c)[i] = {(int32_t)before, r.n - (copy ? 1 : 0), r.from, copy ? r.tail : -1};
+        a.new_lens[i] = r.L + r.g;  // zeroed by the applier when the call is refused
+        before += c;
     }
-    // ---- the pool: copy the counts, find the free pages
-    int64_t nfree = 0;
-    int64_t rank0 = cluster_base<false>(a.ref_in, a.num_pages, s_warp, &s_total, nfree, [&](int64_t at, const int4 &v) {
-        if (a.ref_out == a.ref_in) return;
-        if (at + 4 <= a.num_pages) *reinterpret_cast<int4 *>(a.ref_out + at) = v;
-        else {
-            if (at < a.num_pages) a.ref_out[at] = v.x;
-            if (at + 1 < a.num_pages) a.ref_out[at + 1] = v.y;
-            if (at + 2 < a.num_pages) a.ref_out[at + 2] = v.z;
-        }
-    });
-    const unsigned all_bad = rows_bad | (!rows_bad && need > nfree ? VX_DATA_NO_PAGES : 0u);
-    if (lead) {
-        if (tid == 0) {
-            a.head[0] = all_bad ? 0 : 1;
-            if (all_bad) set_err(a.err, all_bad);
-        }
-        for (int i = tid; i < a.new_rows; i += PG_THREADS) {
-            const int32_t p = a.parent[i];
-            a.new_lens[i] = all_bad ? 0 : (p >= 0 ? a.seq_lens[p] : 0) + a.grow[i];
-        }
-        for (int b = tid; b < a.B; b += PG_THREADS) {
-            a.list_b[b] = s.kids[b] - 1;
-            if (s.kids[b] == 0) a.list_c[b] = -1;
-        }
-    }
-    if (!all_bad) {
-        // ---- hand the lowest `need` free pages to the rows
-        const int64_t span = warp_span(a.num_pages), p0 = ((int64_t)cl.block_rank() * PG_WARPS + warp) * span;
-        for (int64_t o = 0; o < span && rank0 < need; o += 128) {
-            const int64_t at = p0 + o + lane * 4;
-            const uint32_t f = flags4<false>(load4(a.ref_in, at, a.num_pages, -1), at, a.num_pages);
-            int total;
-            int64_t r = rank0 + lane_rank(f, lane, total);
-            rank0 += total;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (!((f >> e) & 1u)) continue;
-                if (r < need) {
-                    const int32_t id = (int32_t)(at + e);
-                    int lo = 0, hi = a.new_rows - 1;  // the last row with off <= r
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (s.off[mid] <= r) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    const int32_t k = (int32_t)r - s.off[lo], p = a.parent[lo];
-                    a.new_indices[a.new_ptr[lo] + s.held[lo] + k] = id;
-                    if (k == 0 && p >= 0 && s.held[lo] < ceil_div(a.seq_lens[p], a.P)) a.list_a[lo] = id;
-                    a.ref_out[id] = 1;
-                }
-                ++r;
-            }
-        }
-    }
-    cl.sync();  // no CTA leaves while another may still read its total
+    for (int b = tid; b < a.B; b += PG_THREADS) a.list_d[b] = s_kids[b];
 }
 
-__global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a) {
+// Blocks of the second kernel by job, in this order, and what one of them is divided into (32-bit:
+// a 64-bit division costs as much as the rest of a block's address arithmetic)
+struct UpdateJobs {
+    uint32_t copies, fresh, rows, refs;
+    uint32_t spans, pieces;
+};
+// false: more blocks or warps than 2^31
+__host__ __forceinline__ bool update_jobs(const PageArgs &a, UpdateJobs *j) {
+    constexpr int64_t W = PG_BLOCK / 32;
+    const int64_t segs = (a.num_pages + PG_SEG - 1) / PG_SEG;
+    const int64_t spans = (a.max_pages + PG_SPAN - 1) / PG_SPAN;
+    const int64_t pieces = (((int64_t)a.kb + a.vb + a.cb) / 16 + PG_PIECE - 1) / PG_PIECE;
+    const int64_t n[4] = {a.new_rows * pieces, (segs * 4 + W - 1) / W, (a.new_rows * spans + W - 1) / W,
+                          (a.B * spans + W - 1) / W};
+    *j = {(uint32_t)n[0], (uint32_t)n[1], (uint32_t)n[2], (uint32_t)n[3], (uint32_t)spans, (uint32_t)pieces};
+    return (n[0] + n[1] + n[2] + n[3]) * W <= INT32_MAX;
+}
+
+__global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a, const UpdateJobs jobs) {
+    __shared__ uint32_t s_pre[PG_GROUPS + 1], s_warp[PG_BLOCK / 32];
+    __shared__ int32_t s_off[PG_MAX_ROWS];
     pdl_wait();
-    if (a.head[0] == 0) return;
-    const int pieces = page_pieces(a);
-    const int spans = ceil_div(a.max_pages, PG_SPAN);
-    const int64_t copies = (int64_t)a.new_rows * pieces, rows = (int64_t)a.new_rows * spans,
-                  refs = (int64_t)a.B * spans;
-    for (int64_t it = blockIdx.x; it < copies + rows + refs; it += gridDim.x) {
-        if (it < copies) {  // the copy of a forked row's last page
-            const int i = (int)(it / pieces);
-            const int32_t d = a.list_a[i];
-            if (d < 0) continue;
-            const int32_t p = a.parent[i];
-            const int32_t src = a.page_indices[a.page_ptr[p] + a.seq_lens[p] / a.P];
-            copy_piece(a, src, d, (int)(it % pieces));
-        } else if (it < copies + rows) {  // entries taken over from the parent
-            const int i = (int)((it - copies) / spans), j0 = (int)((it - copies) % spans) * PG_SPAN;
-            const int32_t p = a.parent[i];
-            if (p < 0) continue;
-            const int held = ceil_div(a.seq_lens[p], a.P) - (a.list_a[i] >= 0 ? 1 : 0);
-            const int32_t *from = a.page_indices + a.page_ptr[p];
-            int32_t *to = a.new_indices + a.new_ptr[i];
-            for (int j = j0 + threadIdx.x; j < min(held, j0 + PG_SPAN); j += PG_BLOCK) to[j] = from[j];
-        } else {  // references of an old row's pages
-            const int b = (int)((it - copies - rows) / spans), j0 = (int)((it - copies - rows) % spans) * PG_SPAN;
-            const int32_t L = a.seq_lens[b], whole = L / a.P, n = ceil_div(L, a.P);
-            const int dw = a.list_b[b], dt = a.list_c[b];
-            if (dw == 0 && (dt == 0 || n == whole)) continue;
-            const int32_t *from = a.page_indices + a.page_ptr[b];
-            for (int j = j0 + threadIdx.x; j < min(n, j0 + PG_SPAN); j += PG_BLOCK) {
-                const int32_t id = from[j];
-                if (id < 0 || id >= a.num_pages) set_err(a.err, VX_DATA_BAD_PAGE_ID);
-                else if (const int d = j < whole ? dw : dt) atomicAdd(a.ref_out + id, d);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const RowPlan *plans = reinterpret_cast<const RowPlan *>(a.list_c);
+    // the block's job, and what its warp works on: a quarter of a segment, a span of a new or an old
+    // row, or a piece of a page.  What can be loaded is on its way before the ranks are summed.
+    uint32_t job = blockIdx.x;
+    const bool is_copy = job < jobs.copies, is_fresh = !is_copy && (job -= jobs.copies) < jobs.fresh,
+               is_row = !is_copy && !is_fresh && (job -= jobs.fresh) < jobs.rows;
+    if (!is_copy && !is_fresh && !is_row) job -= jobs.rows;
+    const uint32_t unit = job * (PG_BLOCK / 32) + (tid >> 5);
+    RowPlan plan{0, 0, 0, -1};
+    int at = 0, item = 0, j0 = 0, kids = 0, L = 0;
+    if (is_copy) {
+        item = job / jobs.pieces;
+        plan = plans[item];
+    } else if (is_row) {
+        item = unit / jobs.spans;
+        j0 = (unit - item * jobs.spans) * PG_SPAN;
+        if (item < a.new_rows) {
+            plan = plans[item];
+            at = a.new_ptr[item];
+        }
+    } else if (!is_fresh) {
+        item = unit / jobs.spans;
+        j0 = (unit - item * jobs.spans) * PG_SPAN;
+        if (item < a.B) {
+            L = a.seq_lens[item];
+            at = a.page_ptr[item];
+            kids = a.list_d[item];
+        }
+    }
+    const uint32_t need = (uint32_t)a.head[1];
+    const unsigned row_bad = (unsigned)a.head[0];
+    const PoolRanks free_pages(a, s_pre, s_warp);
+    const unsigned bad = row_bad ? row_bad : need > free_pages.total() ? VX_DATA_NO_PAGES : 0u;
+    if (bad) {
+        for (uint32_t i = blockIdx.x * PG_BLOCK + tid; i < (uint32_t)a.new_rows; i += gridDim.x * PG_BLOCK) a.new_lens[i] = 0;
+        if (blockIdx.x == 0 && tid == 0) set_err(a.err, bad);
+        return;
+    }
+    if (is_copy) {  // of a forked row's last page
+        if (plan.tail >= 0)
+            copy_piece(a, plan.tail, free_pages.page_of((uint32_t)plan.off, lane), job - item * jobs.pieces);
+    } else if (is_row) {  // entries taken over from the parent
+        int32_t id[PG_SPAN / 32];
+#pragma unroll
+        for (int u = 0; u < PG_SPAN / 32; ++u) {
+            const int j = j0 + 32 * u + lane;
+            if (j < plan.held) id[u] = a.page_indices[plan.from + j];
+        }
+#pragma unroll
+        for (int u = 0; u < PG_SPAN / 32; ++u) {
+            const int j = j0 + 32 * u + lane;
+            if (j < plan.held) a.new_indices[at + j] = id[u];
+        }
+    } else if (!is_fresh) {  // references of an old row's pages
+        const int log2_p = __ffs(a.P) - 1;
+        const int32_t whole = L >> log2_p, n = (L + a.P - 1) >> log2_p;
+        const int dw = (kids >> 1) - 1, dt = (kids & 1) - 1;
+        if (j0 >= n || (dw == 0 && (dt == 0 || n == whole))) return;
+#pragma unroll 4
+        for (int j = j0 + lane; j < min(n, j0 + PG_SPAN); j += 32) {
+            const int32_t id = a.page_indices[at + j];
+            if (id < 0 || id >= a.num_pages) set_err(a.err, VX_DATA_BAD_PAGE_ID);
+            else if (const int d = j < whole ? dw : dt) atomicAdd(a.ref_out + id, d);
+        }
+    } else {  // the lowest `need` free pages to the rows in order
+        const int first = (int)(job * (PG_BLOCK / 32) / 4);
+        if (free_pages.before_segment(min(first, free_pages.segs - 1)) >= need) return;
+        for (int i = tid; i < a.new_rows; i += PG_BLOCK) s_off[i] = plans[i].off;
+        __syncthreads();
+        const int seg = (int)(unit / 4), w0 = (int)(unit % 4) * 8;
+        if (seg >= free_pages.segs) return;
+        uint32_t rank0;
+        const uint32_t words = free_pages.segment_word(seg, lane, rank0);
+#pragma unroll 1
+        for (int w = w0; w < w0 + 8; ++w) {
+            const uint32_t f = __shfl_sync(FULL, words, w);
+            const uint32_t r = __shfl_sync(FULL, rank0, w) + __popc(f & ((1u << lane) - 1u));
+            if (!((f >> lane) & 1u) || r >= need) continue;
+            const int32_t page = seg * PG_SEG + w * 32 + lane;
+            int lo = 0, hi = a.new_rows - 1;  // the last row whose fresh pages start at or before rank r
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((uint32_t)s_off[mid] <= r) lo = mid;
+                else hi = mid - 1;
             }
+            a.new_indices[a.new_ptr[lo] + plans[lo].held + (int32_t)(r - (uint32_t)s_off[lo])] = page;
+            a.ref_out[page] = 1;
         }
     }
 }
 
 // ------------------------------------------------------------------ compaction
 
-// list_a[i]: the i-th free page below n; list_b[r], list_c[r]: id and references of the r-th
-// live page (r >= head[0] only: those with id >= n); head[1]: moves.  Move i takes page
-// list_b[head[0] + i] to list_a[i].
-__global__ void __cluster_dims__(PG_CTAS) __launch_bounds__(PG_THREADS) k_plan_compact(const PageArgs a) {
-    __shared__ int32_t s_warp[PG_WARPS], s_total;
+__global__ void __launch_bounds__(PG_THREADS) k_plan_compact(const PageArgs a) {
     pdl_wait();
     pdl_trigger();
-    cg::cluster_group cl = cg::this_cluster();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t n = 0;
-    int64_t rank0 = cluster_base<true>(a.ref_in, a.num_pages, s_warp, &s_total, n, [](int64_t, const int4 &) {});
-    const int64_t span = warp_span(a.num_pages), p0 = ((int64_t)cl.block_rank() * PG_WARPS + warp) * span;
-#pragma unroll 2
-    for (int64_t o = 0; o < span; o += 128) {
-        const int64_t at = p0 + o + lane * 4;
-        const int4 v = load4(a.ref_in, at, a.num_pages, 0);
-        const int ref[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t f = flags4<true>(v, at, a.num_pages);
-        int total;
-        int64_t r = rank0 + lane_rank(f, lane, total);  // live pages before this one
-        rank0 += total;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t p = at + e;
-            if (p >= a.num_pages) break;
-            const bool live = (f >> e) & 1u;
-            if (p == n) a.head[0] = (int32_t)r;
-            if (p >= n) {
-                if (live) {
-                    a.list_b[r] = (int32_t)p;
-                    a.list_c[r] = ref[e];
-                } else {
-                    a.remap[p] = -1;
-                }
-                a.ref_out[p] = 0;
-            } else if (live) {
-                a.remap[p] = (int32_t)p;
-                a.ref_out[p] = ref[e];
-            } else {
-                a.list_a[p - r] = (int32_t)p;
-                a.remap[p] = -1;
-            }
-            r += live;
-        }
-    }
-    if (n == a.num_pages && cl.block_rank() == 0 && threadIdx.x == 0) a.head[0] = (int32_t)n;
-    cl.sync();
-    const int32_t low = *reinterpret_cast<volatile int32_t *>(a.head), moves = (int32_t)n - low;
-    if (cl.block_rank() == 0 && threadIdx.x == 0) {
-        a.head[1] = moves;
-        *a.num_live = (int32_t)n;
-    }
-    for (int i = (int)cl.block_rank() * PG_THREADS + threadIdx.x; i < moves; i += PG_CTAS * PG_THREADS) {
-        const int32_t d = a.list_a[i];
-        a.remap[a.list_b[low + i]] = d;
-        a.ref_out[d] = a.list_c[low + i];
-    }
-    cl.sync();
+    flag_pages<true>(a, (int64_t)blockIdx.x * PG_THREADS * 4, a.ref_out != a.ref_in ? a.ref_out : nullptr);
 }
 
-__global__ void __launch_bounds__(PG_BLOCK) k_apply_compact(const PageArgs a) {
+// With n live pages, `low` of them below page n: move i takes the live page of rank low + i to the
+// free page of rank i.  list_e[i] is the one, list_f[i] the other; remap[p] of a page that moves is
+// -2 - i until the move writes its new id; head[0] the moves.
+__global__ void __launch_bounds__(PG_BLOCK) k_list_compact(const PageArgs a) {
+    __shared__ uint32_t s_pre[PG_GROUPS + 1], s_warp[PG_BLOCK / 32];
     pdl_wait();
-    const int pieces = page_pieces(a);
-    const int spans = ceil_div(a.max_pages, PG_SPAN);
-    const int32_t low = a.head[0], moves = a.head[1];
-    const int64_t copies = (int64_t)moves * pieces, rows = (int64_t)a.B * spans;
-    for (int64_t it = blockIdx.x; it < copies + rows; it += gridDim.x) {
-        if (it < copies) {
-            const int i = (int)(it / pieces);
-            copy_piece(a, a.list_b[low + i], a.list_a[i], (int)(it % pieces));
-        } else {
-            const int b = (int)((it - copies) / spans), j0 = (int)((it - copies) % spans) * PG_SPAN;
-            const int32_t L = a.seq_lens[b];
-            if (L < 0 || L > a.max_pages * a.P) {
-                if (j0 == 0 && threadIdx.x == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
-                continue;
-            }
-            const int n = ceil_div(L, a.P);
-            const int64_t at = a.page_ptr[b];
-            for (int j = j0 + threadIdx.x; j < min(n, j0 + PG_SPAN); j += PG_BLOCK) {
-                const int32_t id = a.page_indices[at + j];
-                int32_t to = id >= 0 && id < a.num_pages ? a.remap[id] : -1;
-                if (to < 0) {
-                    set_err(a.err, VX_DATA_BAD_PAGE_ID);
-                    to = id;
-                }
-                a.indices_out[at + j] = to;
-            }
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const PoolRanks live(a, s_pre, s_warp);
+    const uint32_t n = live.total();
+    // live pages below page n
+    uint32_t low = n;
+    if (n < a.num_pages) {
+        uint32_t rank;
+        const uint32_t w = live.segment_word((int)(n / PG_SEG), lane, rank);
+        low = __shfl_sync(FULL, rank + __popc(w & ((1u << (n & 31)) - 1u)), (int)(n / 32) & 31);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.head[0] = (int32_t)(n - low);
+        *a.num_live = (int32_t)n;
+    }
+    const int64_t q = (int64_t)blockIdx.x * (PG_BLOCK / 32) + (threadIdx.x >> 5);
+    const int seg = (int)(q / 4), w0 = (int)(q % 4) * 8;
+    if (seg >= live.segs) return;
+    uint32_t rank0;
+    const uint32_t words = live.segment_word(seg, lane, rank0);
+#pragma unroll 1
+    for (int w = w0; w < w0 + 8; ++w) {
+        const uint32_t f = __shfl_sync(FULL, words, w);
+        const uint32_t r = __shfl_sync(FULL, rank0, w) + __popc(f & ((1u << lane) - 1u));
+        const uint32_t p = (uint32_t)seg * PG_SEG + w * 32 + lane;
+        if (p >= a.num_pages) return;
+        const bool is_live = (f >> lane) & 1u;
+        if (is_live && p >= n) a.list_e[r - low] = (int32_t)p;
+        if (!is_live && p < n) a.list_f[p - r] = (int32_t)p;
+        a.remap[p] = !is_live ? -1 : p < n ? (int32_t)p : -2 - (int32_t)(r - low);
+    }
+}
+
+// Blocks [0, rows): tables, a warp to PG_SPAN entries; the others: pieces of the moves
+__global__ void __launch_bounds__(PG_BLOCK) k_apply_compact(const PageArgs a, const int rows) {
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    if ((int)blockIdx.x < rows) {
+        const uint32_t spans = ceil_div(a.max_pages, PG_SPAN);
+        const uint32_t it = blockIdx.x * (PG_BLOCK / 32) + (tid >> 5);
+        const int b = it / spans, j0 = (it - b * spans) * PG_SPAN;
+        if (b >= a.B) return;
+        const int32_t L = a.seq_lens[b];
+        if (L < 0 || L > a.max_pages * a.P) {
+            if (j0 == 0 && lane == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
+            return;
         }
+        const int n = ceil_div(L, a.P);
+        const int64_t at = a.page_ptr[b];
+#pragma unroll 4
+        for (int j = j0 + lane; j < min(n, j0 + PG_SPAN); j += 32) {
+            const int32_t id = a.page_indices[at + j];
+            int32_t to = id >= 0 && id < a.num_pages ? a.remap[id] : -1;
+            if (to < -1) to = a.list_f[-2 - to];  // not written by its move yet
+            if (to < 0) {
+                set_err(a.err, VX_DATA_BAD_PAGE_ID);
+                to = id;
+            }
+            a.indices_out[at + j] = to;
+        }
+        return;
+    }
+    const uint32_t pieces = page_pieces(a), copies = (uint32_t)a.head[0] * pieces;
+    for (uint32_t it = blockIdx.x - rows; it < copies; it += gridDim.x - rows) {
+        const int i = it / pieces, piece = it - i * pieces;
+        const int32_t from = a.list_e[i], to = a.list_f[i];
+        if (piece == 0 && tid == 0) {
+            a.ref_out[to] = a.ref_in[from];
+            a.ref_out[from] = 0;
+            a.remap[from] = to;
+        }
+        copy_piece(a, from, to, piece);
     }
 }
 
@@ -486,35 +564,41 @@ cudaError_t apply_grid(int64_t items, unsigned *grid) {
     return cudaSuccess;
 }
 
-template <typename Plan, typename Apply>
-cudaError_t launch_pages(Plan plan, Apply apply, size_t smem, int64_t items, const PageArgs &a, cudaStream_t s) {
-    unsigned grid = 0;
-    cudaError_t e = apply_grid(items, &grid);
-    if (e == cudaSuccess) e = launch_k(plan, dim3(PG_CTAS), dim3(PG_THREADS), smem, s, true, a);
-    if (e == cudaSuccess) e = launch_k(apply, dim3(grid), dim3(PG_BLOCK), 0, s, true, a);
-    return e;
-}
-
+int64_t plan_blocks(const PageArgs &a) { return (a.num_pages + 4 * PG_THREADS - 1) / (4 * PG_THREADS); }
 int64_t host_pieces(const PageArgs &a) { return (((int64_t)a.kb + a.vb + a.cb) / 16 + PG_PIECE - 1) / PG_PIECE; }
 
 }  // namespace
 
 cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s) {
-    return launch_pages(k_plan_copy, k_apply_copy, 0, (int64_t)a.num_copies * host_pieces(a), a, s);
+    unsigned grid = 0;
+    if (a.num_copies * host_pieces(a) > INT32_MAX) return cudaErrorInvalidValue;
+    cudaError_t e = apply_grid((int64_t)a.num_copies * host_pieces(a), &grid);
+    if (e == cudaSuccess) e = launch_k(k_plan_copy, dim3(PG_CTAS), dim3(PG_THREADS), 0, s, true, a);
+    if (e == cudaSuccess) e = launch_k(k_apply_copy, dim3(grid), dim3(PG_BLOCK), 0, s, true, a);
+    return e;
 }
 
 cudaError_t launch_update_table(const PageArgs &a, cudaStream_t s) {
-    constexpr int smem = 4 * PG_MAX_ROWS * (int)sizeof(int32_t);
-    static std::atomic<unsigned long long> done;
-    const cudaError_t e = ensure_smem_limit(k_plan_update, smem, done);
-    if (e != cudaSuccess) return e;
-    const int64_t spans = (a.max_pages + PG_SPAN - 1) / PG_SPAN;
-    return launch_pages(k_plan_update, k_apply_update, smem, a.new_rows * host_pieces(a) + (a.new_rows + a.B) * spans, a, s);
+    UpdateJobs j;
+    if (!update_jobs(a, &j)) return cudaErrorInvalidValue;
+    const uint32_t blocks = j.fresh + j.rows + j.refs + j.copies;
+    cudaError_t e = launch_k(k_plan_update, dim3((unsigned)(1 + plan_blocks(a))), dim3(PG_THREADS), 0, s, true, a);
+    if (e == cudaSuccess) e = launch_k(k_apply_update, dim3((unsigned)blocks), dim3(PG_BLOCK), 0, s, true, a, j);
+    return e;
 }
 
 cudaError_t launch_compact_pages(const PageArgs &a, cudaStream_t s) {
-    const int64_t spans = (a.max_pages + PG_SPAN - 1) / PG_SPAN;
-    return launch_pages(k_plan_compact, k_apply_compact, 0, a.num_pages / 2 * host_pieces(a) + a.B * spans, a, s);
+    constexpr int W = PG_BLOCK / 32;
+    const int64_t lists = ((a.num_pages + PG_SEG - 1) / PG_SEG * 4 + W - 1) / W;
+    const int64_t rows = (a.B * (int64_t)((a.max_pages + PG_SPAN - 1) / PG_SPAN) + W - 1) / W;
+    unsigned grid = 0;
+    cudaError_t e = apply_grid(std::max<int64_t>(1, a.num_pages / 2 * host_pieces(a)), &grid);
+    if ((rows + grid) * W > INT32_MAX || a.num_pages * host_pieces(a) > INT32_MAX) e = cudaErrorInvalidValue;
+    if (e == cudaSuccess) e = launch_k(k_plan_compact, dim3((unsigned)plan_blocks(a)), dim3(PG_THREADS), 0, s, true, a);
+    if (e == cudaSuccess) e = launch_k(k_list_compact, dim3((unsigned)lists), dim3(PG_BLOCK), 0, s, true, a);
+    if (e == cudaSuccess)
+        e = launch_k(k_apply_compact, dim3((unsigned)(rows + grid)), dim3(PG_BLOCK), 0, s, true, a, (int)rows);
+    return e;
 }
 
 }  // namespace vx

@@ -126,8 +126,10 @@ struct PageArgs {
     int64_t num_indices;
     // compact
     int32_t *indices_out, *remap, *num_live;
-    // workspace: head words, then arrays (see k_pages.cu)
-    int32_t *head, *list_a, *list_b, *list_c;
+    // workspace: head words; copy: list_a [num_pages]; else list_a bits of the pages (32 words for
+    // each segment of 1024), list_b [segments], list_c [4 new_rows], list_d [B], and
+    // list_e, list_f [num_pages / 2] (see k_pages.cu)
+    int32_t *head, *list_a, *list_b, *list_c, *list_d, *list_e, *list_f;
 };
 
 // New tokens request i writes in a prefill: seq_lens[i] - first_pos[i], or none for a request

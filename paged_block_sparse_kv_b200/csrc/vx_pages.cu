@@ -74,26 +74,41 @@ void table_args(vx::PageArgs *a, const vx_geometry *g, const vx_page_table *t) {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// head words, then three lists of as many entries as the pool has pages or a table rows
-size_t list_bytes(const vx_geometry *g, int32_t rows) {
-    return up256((size_t)std::max<int64_t>(g->num_pool_pages, std::max(rows, g->batch)) * sizeof(int32_t));
+// Workspace: head words, a word per page (the copy's claims) or per 32 pages (flags, whole segments
+// of 1024 pages), a count per segment, four words per new row, one per old row, two per possible move.
+struct PageWs {
+    size_t a, b, c, d, e, f, total;
+};
+PageWs page_ws(const vx_geometry *g, int32_t rows) {
+    const size_t n = (size_t)g->num_pool_pages, segs = (n + 1023) / 1024;
+    PageWs w;
+    w.a = 256;
+    w.b = w.a + up256(std::max(n, segs * 32) * sizeof(int32_t));
+    w.c = w.b + up256(segs * sizeof(int32_t));
+    w.d = w.c + up256((size_t)rows * 4 * sizeof(int32_t));
+    w.e = w.d + up256((size_t)g->batch * sizeof(int32_t));
+    w.f = w.e + up256((n / 2 + 1) * sizeof(int32_t));
+    w.total = w.f + up256((n / 2 + 1) * sizeof(int32_t));
+    return w;
 }
-size_t page_ws_bytes(const vx_geometry *g, int32_t rows) { return 256 + 3 * list_bytes(g, rows); }
 
 vx_status set_ws(vx::PageArgs *a, const vx_geometry *g, int32_t rows, void *ws, size_t ws_bytes) {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15u))
         return bad(VX_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
-    if (ws_bytes < page_ws_bytes(g, rows)) {
+    const PageWs w = page_ws(g, rows);
+    if (ws_bytes < w.total) {
         char msg[96];
-        snprintf(msg, sizeof msg, "workspace of %zu bytes < %zu needed", ws_bytes, page_ws_bytes(g, rows));
+        snprintf(msg, sizeof msg, "workspace of %zu bytes < %zu needed", ws_bytes, w.total);
         return set_error(VX_ERR_WORKSPACE, msg);
     }
     char *p = static_cast<char *>(ws);
-    const size_t n = list_bytes(g, rows);
     a->head = reinterpret_cast<int32_t *>(p);
-    a->list_a = reinterpret_cast<int32_t *>(p + 256);
-    a->list_b = reinterpret_cast<int32_t *>(p + 256 + n);
-    a->list_c = reinterpret_cast<int32_t *>(p + 256 + 2 * n);
+    a->list_a = reinterpret_cast<int32_t *>(p + w.a);
+    a->list_b = reinterpret_cast<int32_t *>(p + w.b);
+    a->list_c = reinterpret_cast<int32_t *>(p + w.c);
+    a->list_d = reinterpret_cast<int32_t *>(p + w.d);
+    a->list_e = reinterpret_cast<int32_t *>(p + w.e);
+    a->list_f = reinterpret_cast<int32_t *>(p + w.f);
     return VX_OK;
 }
 
@@ -102,6 +117,12 @@ vx_status launched(cudaError_t e, const char *where) {
     char msg[160];
     snprintf(msg, sizeof msg, "%s: %s", where, cudaGetErrorString(e));
     return set_error(VX_ERR_CUDA, msg);
+}
+
+// The kernels index their work with 31 bits: pieces of 16 KB of a page, spans of 256 table entries.
+int64_t pieces_of(const vx::PageArgs &a) { return (((int64_t)a.kb + a.vb + a.cb) / 16 + 1023) / 1024; }
+vx_status check_work(int64_t units) {
+    return units <= INT32_MAX ? VX_OK : bad(VX_ERR_UNSUPPORTED, "more than 2^31 units of work in one call");
 }
 
 // [a, a + an) and [b, b + bn) share a byte
@@ -120,7 +141,7 @@ size_t vx_page_workspace_size(const vx_geometry *geo, int32_t rows) {
         bad(VX_ERR_INVALID_ARG, "rows must be in [1, 4096]");
         return 0;
     }
-    return page_ws_bytes(geo, rows);
+    return page_ws(geo, rows).total;
 }
 
 vx_status vx_copy_pages(const vx_geometry *geo, const vx_page_pool *src, const vx_page_pool *dst,
@@ -155,6 +176,7 @@ vx_status vx_copy_pages(const vx_geometry *geo, const vx_page_pool *src, const v
     a.num_copies = num_copies;
     a.one_pool = one ? 1 : 0;
     a.err = err;
+    VX_TRY(check_work(num_copies * pieces_of(a)));
     return launched(vx::launch_copy_pages(a, static_cast<cudaStream_t>(stream)), "page copy launch");
 }
 
@@ -199,6 +221,8 @@ vx_status vx_update_table(const vx_geometry *geo, const vx_page_pool *pool, cons
     a.new_lens = new_seq_lens;
     a.new_max_pages = new_max_pages;
     a.err = err;
+    VX_TRY(check_work(8 * (new_rows * pieces_of(a) + 4) + pool->num_pages / 256 +
+                      ((int64_t)new_rows + geo->batch + 2) * (table->max_pages / 256 + 1)));
     return launched(vx::launch_update_table(a, static_cast<cudaStream_t>(stream)), "table update launch");
 }
 
@@ -229,6 +253,7 @@ vx_status vx_compact_pages(const vx_geometry *geo, const vx_page_pool *pool, con
     a.remap = remap;
     a.num_live = num_live;
     a.err = err;
+    VX_TRY(check_work(pool->num_pages * pieces_of(a) + ((int64_t)geo->batch + 2) * (table->max_pages / 256 + 1) + (1 << 20)));
     return launched(vx::launch_compact_pages(a, static_cast<cudaStream_t>(stream)), "page compaction launch");
 }
 

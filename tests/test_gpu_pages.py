@@ -263,6 +263,9 @@ def test_update_refusals_change_nothing():
     refused([0], [0], vx.VX_DATA_BAD_ROW, ptr=np.array([62]))
     refused([0], [0], vx.VX_DATA_BAD_ROW, ptr=np.array([-1]))
     refused([0], [0], vx.VX_DATA_BAD_PAGE_ID, lens=[47, 48, 96], tail=12)
+    r.ref[r.rows[0][-1]] = 0  # a last page that its own row holds and the counts call free
+    base = (base[0], r.ref.copy())
+    refused([0], [0], vx.VX_DATA_BAD_PAGE_ID, lens=[47, 48, 96])
 
 
 # ------------------------------------------------------------------------------------------------ compaction
