@@ -8,11 +8,16 @@
 // sum of up to 64 codes exact in fp32 (int8: integers; e4m3: multiples of 2^-9 below 2^15),
 // product and quotient in fp64, one rounding.
 //
-// One unit is the keys or the values of one (page, KV head).  Its page_size / 16 warps hold 16
-// token rows each in registers (a lane: 16-byte chunks of rows, as they lie in memory), take
-// the largest magnitude with a warp reduction (and through shared memory when the unit has
-// several warps), convert, and store; nothing is read twice.  HBM bound: 2 bytes read and 1
-// written per element.
+// One unit is the keys or the values of one (page, KV head).
+//  * A page that holds new tokens alone (all but the first page of a prefill chunk): the unit's
+//    page_size / 16 warps keep 16 token rows each in registers (a lane: 16-byte chunks of rows),
+//    take the largest magnitude with a warp reduction (and through shared memory when the unit
+//    has several warps), convert, store; nothing is read twice.  HBM bound: 2 bytes read and 1
+//    written per element.
+//  * A page that holds older tokens too: the same warps with its codes in registers as well.
+//  * Append: a warp per unit; the one new row, and for the centroid the page's key codes in
+//    16-byte chunks.  Value codes are read only when the scale grows.  Latency bound (length ->
+//    table -> codes).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -52,7 +57,168 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
     return __uint_as_float((e > n ? e - n : 1u) << 23);  // fp32 exponent field, 1 at least
 }
 
-// One unit, by its WPU warps (this warp: rows [16 * part, 16 * part + 16)).  Rows [0, n_old) are
+// Four new elements (floats x0..x3, |x * inv| <= qmax) to code bytes; int8: `bits` of the sums are
+// added up for the centroid, see below.
+template <int FMT>
+__device__ __forceinline__ uint32_t four_codes(float x0, float x1, float x2, float x3, float inv, uint32_t (&b)[4]) {
+    if constexpr (FMT == VX_QUANT_INT8) {
+        // 1.5 * 2^23 + x rounds x to an integer, ties to even, in the low bits: 0x4b400000 + code
+        b[0] = __float_as_uint(fmaf(x0, inv, 12582912.f));
+        b[1] = __float_as_uint(fmaf(x1, inv, 12582912.f));
+        b[2] = __float_as_uint(fmaf(x2, inv, 12582912.f));
+        b[3] = __float_as_uint(fmaf(x3, inv, 12582912.f));
+        return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 * inv, x1 * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2 * inv, x3 * inv), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+}
+
+// bf16(s * sum / m), rounded once.  A whole page (m a power of two) under a power-of-two scale of
+// ordinary size needs no division: scaling is exact.
+__device__ __forceinline__ uint32_t centroid_bits(float s, float sum, int m) {
+    if ((m & (m - 1)) == 0 && (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-80f && s <= 0x1p80f)
+        return __bfloat16_as_ushort(__float2bfloat16_rn(sum * (s / static_cast<float>(m))));
+    return f64_to_bf16_rne((double)s * sum / m);
+}
+
+// An infinity becomes the largest finite value of its sign, a NaN zero; returns the new largest
+// magnitude.
+template <int NR>
+__device__ __noinline__ uint32_t make_finite(uint4 (&x)[NR]) {
+    uint32_t amax = 0;
+    for (int i = 0; i < NR; ++i) {
+        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h[2] = {w[j] & 0xffffu, w[j] >> 16};
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t mag = h[u] & 0x7fffu;
+                if (mag > 0x7f80u) h[u] = 0;
+                else if (mag == 0x7f80u) h[u] = (h[u] & 0x8000u) | 0x7f7fu;
+                amax = max(amax, h[u] & 0x7fffu);
+            }
+            w[j] = h[0] | (h[1] << 16);
+        }
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return amax;
+}
+
+// Largest magnitude (bf16 bits) of a warp's new rows, made finite.
+template <int NR>
+__device__ __forceinline__ uint32_t largest(uint4 (&x)[NR], int32_t *err, int lane) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const uint32_t a = __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu);
+        const uint32_t b = __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu);
+        top = __vmaxu2(top, __vmaxu2(a, b));
+    }
+    uint32_t amax = __reduce_max_sync(FULL, max(top & 0xffffu, top >> 16));
+    if (amax >= 0x7f80u) {
+        if (lane == 0) set_err(err, VX_DATA_BAD_VALUE);
+        uint4 y[NR];  // a copy, so that x stays in registers on the usual path
+#pragma unroll
+        for (int i = 0; i < NR; ++i) y[i] = x[i];
+        amax = __reduce_max_sync(FULL, make_finite<NR>(y));
+#pragma unroll
+        for (int i = 0; i < NR; ++i) x[i] = y[i];
+    }
+    return amax;
+}
+
+// One unit of a page without older tokens, by its WPU warps (this warp: rows [16 * part, 16 * part +
+// 16) of m); every warp of the block takes part in the barriers, `go`: the unit exists.
+template <int D, int WPU, int FMT, typename RowF, typename PageF>
+__device__ __forceinline__ void quant_new_unit(bool go, bool is_key, int part, RowF new_row, PageF page, int m,
+                                               int32_t *err, int lane, uint32_t *s_max, float (*s_sum)[D]) {
+    constexpr int CPR = D / 8, RPL = 32 / CPR, NR = 16 / RPL;
+    const int chunk = lane % CPR, t0 = part * 16 + lane / CPR;
+    uint4 x[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (go && t0 + i * RPL < m) x[i] = ld_nc_v4(new_row(t0 + i * RPL) + chunk * 8);
+    }
+    uint8_t *codes;
+    float *scale;
+    __nv_bfloat16 *cen;
+    go = page(codes, scale, cen) && go;
+    uint32_t amax = largest<NR>(x, err, lane);
+    if constexpr (WPU > 1) {
+        if (lane == 0) s_max[threadIdx.x >> 5] = amax;
+        __syncthreads();
+        const int first = (threadIdx.x >> 5) - part;
+#pragma unroll
+        for (int w = 0; w < WPU; ++w) amax = max(amax, s_max[first + w]);
+    }
+    const float s = scale_of<FMT>(amax), inv = 1.f / s;
+    uint32_t isum[8];
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        isum[e] = 0u;
+        sum[e] = 0.f;
+    }
+    if (go) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            float f[8];
+            bf16x8_to_f32(x[i], f);
+            uint32_t b[2][4] = {};
+            const uint2 c = make_uint2(four_codes<FMT>(f[0], f[1], f[2], f[3], inv, b[0]),
+                                       four_codes<FMT>(f[4], f[5], f[6], f[7], inv, b[1]));
+            if (t0 + i * RPL < m) *reinterpret_cast<uint2 *>(codes + (t0 + i * RPL) * D + chunk * 8) = c;
+            if (is_key) {  // rows past m are zeros
+                if constexpr (FMT == VX_QUANT_INT8) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) isum[e] += b[e >> 2][e & 3];
+                } else {
+                    const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e]), __NV_E4M3));
+                        sum[2 * e] += __low2float(h);
+                        sum[2 * e + 1] += __high2float(h);
+                    }
+                }
+            }
+        }
+    }
+    if (go && part == 0 && lane == 0) *scale = s;
+    if (WPU == 1 && !is_key) return;
+    if constexpr (FMT == VX_QUANT_INT8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = static_cast<float>(static_cast<int32_t>(isum[e] - NR * 0x4b400000u));
+    }
+#pragma unroll
+    for (int off = CPR; off < 32; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor_sync(FULL, sum[e], off);
+    if constexpr (WPU > 1) {
+        if (lane < CPR) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_sum[threadIdx.x >> 5][chunk * 8 + e] = sum[e];
+        }
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int w = 1; w < WPU; ++w)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += s_sum[(threadIdx.x >> 5) + w][chunk * 8 + e];
+        }
+        __syncthreads();  // s_max and s_sum are free again
+    }
+    if (go && part == 0 && is_key && lane < CPR) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = centroid_bits(s, sum[2 * e], m) | (centroid_bits(s, sum[2 * e + 1], m) << 16);
+        *reinterpret_cast<uint4 *>(cen + chunk * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// One unit of a page with older tokens, by its WPU warps (this warp: rows [16 * part, 16 * part + 16)).  Rows [0, n_old) are
 // the page's older tokens, [n_old, m) come from new_row(t).  `go`: the unit exists (warps of
 // missing units only take part in the block barriers).
 template <int D, int WPU, int FMT, typename RowF>
@@ -82,36 +248,7 @@ __device__ __forceinline__ void quant_unit(bool go, bool is_key, int part, RowF 
                 if (t0 + i * RPL < n_old) old[i] = *reinterpret_cast<const uint2 *>(codes + (t0 + i * RPL) * D + chunk * 8);
         }
     }
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const uint32_t a = __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu);
-        const uint32_t b = __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu);
-        const uint32_t c = __vmaxu2(a, b);
-        amax = max(amax, max(c & 0xffffu, c >> 16));
-    }
-    amax = __reduce_max_sync(FULL, amax);
-    if (amax >= 0x7f80u) {  // an infinity becomes the largest finite value, a NaN zero
-        if (lane == 0) set_err(err, VX_DATA_BAD_VALUE);
-        amax = 0;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t h[2] = {w[j] & 0xffffu, w[j] >> 16};
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t mag = h[u] & 0x7fffu;
-                    if (mag > 0x7f80u) h[u] = 0;
-                    else if (mag == 0x7f80u) h[u] = (h[u] & 0x8000u) | 0x7f7fu;
-                    amax = max(amax, h[u] & 0x7fffu);
-                }
-                w[j] = h[0] | (h[1] << 16);
-            }
-            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        amax = __reduce_max_sync(FULL, amax);
-    }
+    amax = largest<NR>(x, err, lane);
     if constexpr (WPU > 1) {
         if (lane == 0) s_max[threadIdx.x >> 5] = amax;
         __syncthreads();
@@ -189,105 +326,240 @@ __device__ __forceinline__ void quant_unit(bool go, bool is_key, int part, RowF 
         if (is_key && lane < CPR) {
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = f64_to_bf16_rne((double)s * sum[2 * e] / m);
-                const uint32_t hi = f64_to_bf16_rne((double)s * sum[2 * e + 1] / m);
-                w[e] = lo | (hi << 16);
-            }
+            for (int e = 0; e < 4; ++e) w[e] = centroid_bits(s, sum[2 * e], m) | (centroid_bits(s, sum[2 * e + 1], m) << 16);
             *reinterpret_cast<uint4 *>(cen + chunk * 8) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
 
-// Prefill write: grid (ceil(max_pages / QZ_PAGES_PER_BLOCK), B), from the page holding first_pos[b]
-// on.  Append: grid (ceil(2 Hkv WPU / QZ_WARPS), B), first_pos = L - 1, one new row per request.
-template <int D, int WPU, int FMT, bool APPEND>
-__global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_update(const CentroidArgs a, const QuantArgs qa) {
+// Prefill write: grid (ceil(max_pages / QZ_PAGES_PER_BLOCK), B), pages from the one holding first_pos[b]
+// on.  Request b's new rows start in the packed input after those of requests 0..b-1.
+template <int D, int WPU, int FMT>
+__global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_prefill(const CentroidArgs a, const QuantArgs qa) {
     constexpr int UNITS = QZ_WARPS / WPU;  // units in flight per block
     __shared__ uint32_t s_max[QZ_WARPS];
     __shared__ float s_sum[WPU > 1 ? QZ_WARPS : 1][D];
+    __shared__ long long s_part[QZ_WARPS];
     const int b = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // a dependent scorer (vx_block_topk_decode_append_quant) may launch now; it waits for this
-    // grid's end and writes before it reads anything
-    if constexpr (APPEND) pdl_trigger();
-    int64_t row0 = b;  // packed row of request b's first new token
-    const int32_t L = a.seq_lens[b];
-    int32_t fp = L - 1;
-    if constexpr (!APPEND) {
-        __shared__ long long s_part[QZ_WARPS];
-        long long part = 0;
-        for (int i = threadIdx.x; i < b; i += blockDim.x) part += prefill_count(a, i);
+    const int32_t L = a.seq_lens[b], fp = a.first_pos[b];
+    const int n = ceil_div(L, a.P), j_lo = fp / a.P + (int)blockIdx.x * QZ_PAGES_PER_BLOCK;
+    const bool sound = L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L;
+    if (sound && blockIdx.x > 0 && j_lo >= n) return;  // (block 0 checks the input's rows)
+    long long before = 0;
+    for (int i = threadIdx.x; i < b; i += blockDim.x) before += prefill_count(a, i);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(FULL, part, off);
-        if (lane == 0) s_part[warp] = part;
-        __syncthreads();
-        row0 = 0;
+    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(FULL, before, off);
+    if (lane == 0) s_part[warp] = before;
+    __syncthreads();
+    int64_t row0 = 0;
 #pragma unroll
-        for (int w = 0; w < QZ_WARPS; ++w) row0 += s_part[w];
-        fp = a.first_pos[b];
-    }
-    if (L < 1 || L > a.max_pages * a.P || fp < 0 || fp > L || (!APPEND && row0 + (L - fp) > qa.num_new)) {
+    for (int w = 0; w < QZ_WARPS; ++w) row0 += s_part[w];
+    if (!sound || row0 + (L - fp) > qa.num_new) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
         return;
     }
-    const int n = ceil_div(L, a.P);
-    const int j_lo = fp / a.P + (APPEND ? 0 : blockIdx.x * QZ_PAGES_PER_BLOCK);
-    const int j_hi = APPEND ? j_lo + 1 : min(n, j_lo + QZ_PAGES_PER_BLOCK);
     if (fp == L || j_lo >= n) return;
-    const int items = (j_hi - j_lo) * a.Hkv * 2;
+    const int heads2 = a.Hkv * 2, items = (min(n, j_lo + QZ_PAGES_PER_BLOCK) - j_lo) * heads2;
+    const int32_t *table = a.page_indices + a.page_ptr[b];
     const auto *kn = static_cast<const __nv_bfloat16 *>(a.k_new);
     const auto *vn = static_cast<const __nv_bfloat16 *>(a.v_new);
     auto *cen = static_cast<__nv_bfloat16 *>(a.centroids);
-    const int it_lo = APPEND ? blockIdx.x * UNITS : 0;
-    const int it_hi = APPEND ? min(items, it_lo + UNITS) : items;
-    for (int it0 = it_lo; it0 < it_hi; it0 += UNITS) {
+    // the items of a page that holds older tokens come first: the block's page 0, if any
+    const int old_items = j_lo * a.P < fp ? heads2 : 0;
+    for (int it0 = 0; it0 < items; it0 += UNITS) {
         const int it = it0 + warp / WPU;
-        bool go = it < it_hi;
-        const int j = j_lo + (go ? it / (2 * a.Hkv) : 0), rem = go ? it % (2 * a.Hkv) : 0;
+        const bool go = it < items;
+        const int j = j_lo + (go ? it / heads2 : 0), rem = go ? it % heads2 : 0;
         const bool is_key = rem < a.Hkv;
         const int h = is_key ? rem : rem - a.Hkv;
-        int32_t phys = go ? a.page_indices[a.page_ptr[b] + j] : 0;
-        if (phys < 0 || phys >= a.num_pool_pages) {
-            if (lane == 0) set_err(a.err, VX_DATA_BAD_PAGE_ID);
-            go = false;
-            phys = 0;
-        }
         const int m = min(a.P, L - j * a.P);
-        const int n_old = max(0, fp - j * a.P);
-        const size_t blk = (size_t)phys * a.Hkv + h;
         const __nv_bfloat16 *src = (is_key ? kn : vn) + ((row0 + (int64_t)j * a.P - fp) * a.Hkv + h) * D;
-        quant_unit<D, WPU, FMT>(
-            go, is_key, warp % WPU, [&](int t) { return src + (int64_t)t * a.Hkv * D; },
-            (is_key ? qa.k_cache : qa.v_cache) + blk * a.P * D, (is_key ? qa.k_scale : qa.v_scale) + blk,
-            cen + blk * D, n_old, m, a.err, lane, s_max, s_sum);
+        auto new_row = [&](int t) { return src + (int64_t)t * a.Hkv * D; };
+        const int32_t id = table[j];
+        auto page = [&](uint8_t *&codes, float *&scale, __nv_bfloat16 *&centroid) {
+            const bool ok = id >= 0 && id < a.num_pool_pages;
+            if (!ok && go && lane == 0) set_err(a.err, VX_DATA_BAD_PAGE_ID);
+            const size_t blk = (size_t)(ok ? id : 0) * a.Hkv + h;
+            codes = (is_key ? qa.k_cache : qa.v_cache) + blk * a.P * D;
+            scale = (is_key ? qa.k_scale : qa.v_scale) + blk;
+            centroid = cen + blk * D;
+            return ok;
+        };
+        if (it0 < old_items) {  // whole block: old_items and UNITS are powers of two (UNITS may hold new pages too)
+            uint8_t *codes;
+            float *scale;
+            __nv_bfloat16 *centroid;
+            const bool ok = page(codes, scale, centroid) && go;
+            quant_unit<D, WPU, FMT>(ok, is_key, warp % WPU, new_row, codes, scale, centroid, max(0, fp - j * a.P), m,
+                                    a.err, lane, s_max, s_sum);
+        } else {
+            quant_new_unit<D, WPU, FMT>(go, is_key, warp % WPU, new_row, page, m, a.err, lane, s_max, s_sum);
+        }
     }
 }
 
-template <int D, int WPU, int FMT>
-cudaError_t launch_qdwf(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s) {
+// Append: grid (ceil(2 Hkv / QZ_WARPS), B), a warp per unit.  A lane holds 16 codes (D / 16 lanes to
+// a row) of every RPL-th row, and the new row's elements that belong to them.
+template <int D, int NR, int FMT>
+__global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_append(const CentroidArgs a, const QuantArgs qa) {
+    // a dependent scorer (vx_block_topk_decode_append_quant) may launch now; it waits for this
+    // grid's end and writes before it reads anything
+    pdl_trigger();
+    constexpr int CPR = D / 16, RPL = 32 / CPR;
+    const int b = blockIdx.y, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x * QZ_WARPS + (threadIdx.x >> 5);
+    if (unit >= 2 * a.Hkv) return;
+    const bool is_key = unit < a.Hkv;
+    const int h = is_key ? unit : unit - a.Hkv;
+    const int chunk = lane % CPR, t0 = lane / CPR;
+    const auto *src = static_cast<const __nv_bfloat16 *>(is_key ? a.k_new : a.v_new) + ((size_t)b * a.Hkv + h) * D + chunk * 16;
+    uint4 x[2] = {ld_nc_v4(src), ld_nc_v4(src + 8)};
+    const int32_t L = a.seq_lens[b], row = a.page_ptr[b];
+    if (L < 1 || L > a.max_pages * a.P) {
+        if (unit == 0 && lane == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
+        return;
+    }
+    const int slot = (L - 1) & (a.P - 1);
+    const int32_t id = a.page_indices[row + (L - 1) / a.P];
+    if (id < 0 || id >= a.num_pool_pages) {
+        if (lane == 0) set_err(a.err, VX_DATA_BAD_PAGE_ID);
+        return;
+    }
+    const size_t blk = (size_t)id * a.Hkv + h;
+    uint8_t *codes = (is_key ? qa.k_cache : qa.v_cache) + blk * a.P * D + chunk * 16;
+    float *scale = (is_key ? qa.k_scale : qa.v_scale) + blk;
+    const float s_old = slot > 0 ? *scale : 0.f;
+    uint4 old[NR];
+    auto load_old = [&]() {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            old[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t0 + i * RPL < slot) old[i] = *reinterpret_cast<const uint4 *>(codes + (t0 + i * RPL) * D);
+        }
+    };
+    if (is_key) load_old();
+    const uint32_t amax = largest<2>(x, a.err, lane);
+    const float s = fmaxf(scale_of<FMT>(amax), s_old), inv = 1.f / s;
+    float f[16];
+    bf16x8_to_f32(x[0], reinterpret_cast<float(&)[8]>(f));
+    bf16x8_to_f32(x[1], reinterpret_cast<float(&)[8]>(f[8]));
+    uint32_t c[4], bits[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = four_codes<FMT>(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3], inv, bits);
+    if (slot > 0 && s > s_old) {  // the older codes in the new scale
+        if (!is_key) load_old();
+        const float ratio = s_old / s;
+#pragma unroll 1
+        for (int i = 0; i < NR; ++i) {
+            if (t0 + i * RPL >= slot) break;
+            uint32_t w[4];
+            const uint4 o = *reinterpret_cast<const uint4 *>(codes + (t0 + i * RPL) * D);
+            const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    w[e] |= float_to_code<FMT>(code_to_float<FMT>((v[e] >> (8 * u)) & 0xff) * ratio) << (8 * u);
+            }
+            *reinterpret_cast<uint4 *>(codes + (t0 + i * RPL) * D) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (is_key) load_old();  // this lane's own stores
+    }
+    const bool owner = t0 == slot % RPL;  // of the new row's chunk
+    if (owner) *reinterpret_cast<uint4 *>(codes + slot * D) = make_uint4(c[0], c[1], c[2], c[3]);
+    if (lane == 0) *scale = s;
+    if (!is_key) return;
+    // sums of the codes, 16 columns per lane
+    float sum[16];
+    if constexpr (FMT == VX_QUANT_INT8) {
+        // code + 128 in 16-bit halves: at most 64 rows of 255
+        uint32_t even[4] = {}, odd[4] = {};
+        auto add = [&](const uint32_t (&w)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t u = w[e] ^ 0x80808080u;
+                even[e] += u & 0x00ff00ffu;
+                odd[e] += (u >> 8) & 0x00ff00ffu;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (t0 + i * RPL < slot) {
+                const uint32_t w[4] = {old[i].x, old[i].y, old[i].z, old[i].w};
+                add(w);
+            }
+        if (owner) add(c);
+#pragma unroll
+        for (int off = CPR; off < 32; off <<= 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                even[e] += __shfl_xor_sync(FULL, even[e], off);
+                odd[e] += __shfl_xor_sync(FULL, odd[e], off);
+            }
+        const int bias = 128 * (slot + 1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sum[4 * e] = static_cast<float>((int)(even[e] & 0xffffu) - bias);
+            sum[4 * e + 1] = static_cast<float>((int)(odd[e] & 0xffffu) - bias);
+            sum[4 * e + 2] = static_cast<float>((int)(even[e] >> 16) - bias);
+            sum[4 * e + 3] = static_cast<float>((int)(odd[e] >> 16) - bias);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+        auto add = [&](const uint32_t (&w)[4]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t v = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                const __half2 h2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3));
+                sum[2 * e] += __low2float(h2);
+                sum[2 * e + 1] += __high2float(h2);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const uint32_t w[4] = {old[i].x, old[i].y, old[i].z, old[i].w};  // zeros past the older rows
+            add(w);
+        }
+        if (owner) add(c);
+#pragma unroll
+        for (int off = CPR; off < 32; off <<= 1)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e] += __shfl_xor_sync(FULL, sum[e], off);
+    }
+    // every row lane holds all 16 sums: row lane r writes words r, r + RPL, ... of the chunk's 8
+    auto *cen = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.centroids) + blk * D + chunk * 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e % RPL == t0) cen[e] = centroid_bits(s, sum[2 * e], slot + 1) | (centroid_bits(s, sum[2 * e + 1], slot + 1) << 16);
+}
+
+template <int D, int P, int FMT>
+cudaError_t launch_qdpf(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s) {
     if (mode == CEN_APPEND) {
-        const dim3 grid((2 * a.Hkv * WPU + QZ_WARPS - 1) / QZ_WARPS, a.B);
-        k_quant_update<D, WPU, FMT, true><<<grid, QZ_WARPS * 32, 0, s>>>(a, qa);
+        const dim3 grid((2 * a.Hkv + QZ_WARPS - 1) / QZ_WARPS, a.B);
+        k_quant_append<D, P * D / 512, FMT><<<grid, QZ_WARPS * 32, 0, s>>>(a, qa);
     } else {
         const dim3 grid((a.max_pages + QZ_PAGES_PER_BLOCK - 1) / QZ_PAGES_PER_BLOCK, a.B);
-        k_quant_update<D, WPU, FMT, false><<<grid, QZ_WARPS * 32, 0, s>>>(a, qa);
+        k_quant_prefill<D, P / 16, FMT><<<grid, QZ_WARPS * 32, 0, s>>>(a, qa);
     }
     return cudaGetLastError();
 }
 
-template <int D, int WPU>
-cudaError_t launch_qdw(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s) {
-    return qa.format == VX_QUANT_INT8 ? launch_qdwf<D, WPU, VX_QUANT_INT8>(a, qa, mode, s)
-                                      : launch_qdwf<D, WPU, VX_QUANT_E4M3>(a, qa, mode, s);
+template <int D, int P>
+cudaError_t launch_qdp(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s) {
+    return qa.format == VX_QUANT_INT8 ? launch_qdpf<D, P, VX_QUANT_INT8>(a, qa, mode, s)
+                                      : launch_qdpf<D, P, VX_QUANT_E4M3>(a, qa, mode, s);
 }
 
 template <int D>
 cudaError_t launch_qd(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s) {
     switch (a.P) {
-        case 16: return launch_qdw<D, 1>(a, qa, mode, s);
-        case 32: return launch_qdw<D, 2>(a, qa, mode, s);
-        case 64: return launch_qdw<D, 4>(a, qa, mode, s);
+        case 16: return launch_qdp<D, 16>(a, qa, mode, s);
+        case 32: return launch_qdp<D, 32>(a, qa, mode, s);
+        case 64: return launch_qdp<D, 64>(a, qa, mode, s);
         default: return cudaErrorInvalidValue;
     }
 }
