@@ -33,10 +33,12 @@ namespace vx {
 namespace {
 
 constexpr float DQ_PSHIFT = 15.f;  // weights are at most 2^15, fp16's largest number is 65504
-constexpr int DQ_STAGES = 6;  // 16-token tiles in flight per warp (4 KB each at head_dim 128)
+constexpr float DQ_VMIN = 0x1p-126f;  // v_ref of a row without a tile: the smallest normal number
+// 16-token tiles in flight per warp (4 KB each at head_dim 128): about 192 KB per SM
+constexpr int dq_stages(int warps) { return warps > 8 ? 48 / warps : 6; }
 
-struct QuantMeta {
-    int32_t row, nvalid, piece;
+struct __align__(16) QuantMeta {
+    int32_t row, nvalid;
     float ks, vs;
 };
 
@@ -86,92 +88,140 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
     return v;
 }
 
-// One 16-token tile.  qf: the query heads as mma B fragments in the dims order above; hs: the
-// logits' scale of heads 2 q4, 2 q4 + 1 (log2 units); acc: unnormalised output.
-template <int D, int NT, int FMT>
-__device__ __forceinline__ void attend_codes(uint32_t sK, uint32_t sV, int nvalid, float ks, float vs,
-                                             const uint32_t (&qf)[NT][D / 16][2], const float (&hs)[NT][2],
-                                             float (&acc)[NT][D / 16][4], float (&m_run)[NT][2],
-                                             float (&l_run)[NT][2], int lane) {
+// A tile as the consumer sees it: where its codes are, its valid tokens and its page's scales.
+struct Tile {
+    uint32_t k, v;
+    int32_t nvalid;
+    float ks, vs;
+};
+
+// T 16-token tiles of one row.  qf: the query heads as mma B fragments in the dims order above; hs:
+// the logits' scale of heads 2 q4, 2 q4 + 1 (log2 units).  acc: the output, unnormalised, in units
+// of v_ref, the largest |v_scale| met so far: P is multiplied by v_scale / v_ref before it is
+// rounded, so acc needs no multiplication per tile; it is rescaled when the running maximum or
+// v_ref moves, which after a row's first tiles is rare.  (A page whose scale is below 2^-29 of
+// v_ref has its weights rounded as subnormal numbers: an error of at most 2^-40 of the largest
+// weight times v_ref.)  Two tiles at a time share the maximum's shuffles and give the scheduler
+// two independent chains.
+template <int D, int NT, int FMT, int T>
+__device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32_t (&qf)[NT][D / 16][2],
+                                             const float (&hs)[NT][2], float (&acc)[NT][D / 16][4],
+                                             float (&m_run)[NT][2], float (&l_run)[NT][2], float &v_ref, float &v_inv,
+                                             int lane) {
     constexpr int MT = D / 16;
     constexpr int HALVES = D / 64;  // 16-byte chunks a lane takes of a token row
     const int g4 = lane >> 2, q4 = lane & 3;
-    float s[NT][4];
+    float s[T][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][nt][e] = 0.f;
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-        // chunk HALVES * q4 + h: the 8 lanes of a quarter warp cover all 32 banks
-        const uint4 r0 = lds_v4(sK + code_off<D>(g4, HALVES * q4 + h));
-        const uint4 r1 = lds_v4(sK + code_off<D>(g4 + 8, HALVES * q4 + h));
-        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-            uint32_t a0, a1, a2, a3;
-            codes_to_half<FMT, false>(w0[st], a0, a2);
-            codes_to_half<FMT, false>(w1[st], a1, a3);
+        for (int t = 0; t < T; ++t) {
+            // chunk HALVES * q4 + h: the 8 lanes of a quarter warp cover all 32 banks
+            const uint4 r0 = lds_v4(tile[t].k + code_off<D>(g4, HALVES * q4 + h));
+            const uint4 r1 = lds_v4(tile[t].k + code_off<D>(g4 + 8, HALVES * q4 + h));
+            const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][h * 4 + st][0], qf[nt][h * 4 + st][1]);
+            for (int st = 0; st < 4; ++st) {
+                uint32_t a0, a1, a2, a3;
+                codes_to_half<FMT, false>(w0[st], a0, a2);
+                codes_to_half<FMT, false>(w1[st], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16_16816(s[t][nt], a0, a1, a2, a3, qf[nt][h * 4 + st][0], qf[nt][h * 4 + st][1]);
+            }
         }
     }
+    // v_ref of these tiles
+    float v_top = v_ref;
+#pragma unroll
+    for (int t = 0; t < T; ++t) v_top = fmaxf(v_top, fabsf(tile[t].vs));
+    float v_alpha = 1.f;
+    if (v_top > v_ref) {
+        v_alpha = v_ref / v_top;
+        v_ref = v_top;
+        v_inv = 1.f / v_top;
+    }
     // online softmax (base 2), tokens >= nvalid masked
-    uint32_t pb[NT][2];
+    uint32_t pb[T][NT][2];
     float alpha[NT][2];
+    bool moved = v_alpha != 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+        float x[T][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int tok = g4 + 8 * (e >> 1);
-            x[e] = tok < nvalid ? s[nt][e] * (hs[nt][e & 1] * ks) : -INFINITY;
+        for (int t = 0; t < T; ++t) {
+            const float f[2] = {hs[nt][0] * tile[t].ks, hs[nt][1] * tile[t].ks};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[t][e] = g4 + 8 * (e >> 1) < tile[t].nvalid ? s[t][nt][e] * f[e & 1] : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float mx = fmaxf(x[i], x[i + 2]);
+            float mx = fmaxf(x[0][i], x[0][i + 2]);
+#pragma unroll
+            for (int t = 1; t < T; ++t) mx = fmaxf(mx, fmaxf(x[t][i], x[t][i + 2]));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
             const float m_new = fmaxf(m_run[nt][i], mx);
             alpha[nt][i] = exp2f(m_run[nt][i] - m_new);
+            moved |= alpha[nt][i] != 1.f;
             m_run[nt][i] = m_new;
+            l_run[nt][i] *= alpha[nt][i];
+            alpha[nt][i] *= v_alpha;
         }
-        float p[4];
+        const float m0[2] = {m_run[nt][0] - DQ_PSHIFT, m_run[nt][1] - DQ_PSHIFT};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = exp2f(x[e] - (m_run[nt][e & 1] - DQ_PSHIFT));
+        for (int t = 0; t < T; ++t) {
+            const float r = tile[t].vs * v_inv;
+            float p[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) l_run[nt][i] = l_run[nt][i] * alpha[nt][i] + p[i] + p[i + 2];
-        pb[nt][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
-        pb[nt][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
+            for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - m0[e & 1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) l_run[nt][i] += p[i] + p[i + 2];
+            pb[t][nt][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0] * r, p[1] * r)));
+            pb[t][nt][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2] * r, p[3] * r)));
+        }
     }
-    // O^T[dim][head] = alpha * O^T + v_scale * (codes . P^T)
+    if (__any_sync(FULL, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][mt][e] *= alpha[nt][e & 1];
+    }
+    // O^T[dim][head] += codes . P^T
     const int mi = lane >> 3, tok = (lane & 7) + 8 * (mi & 1);
-    const bool tail = nvalid < DEC_TILE;
-    const int t_lo = 2 * q4, t_hi = 8 + 2 * q4;  // tokens of this lane's A halves
-    const uint32_t mlo = (t_lo < nvalid ? 0x0000ffffu : 0u) | (t_lo + 1 < nvalid ? 0xffff0000u : 0u);
-    const uint32_t mhi = (t_hi < nvalid ? 0x0000ffffu : 0u) | (t_hi + 1 < nvalid ? 0xffff0000u : 0u);
 #pragma unroll
-    for (int c = 0; c < MT; c += 2) {
-        uint32_t r[4];
-        ldsm_x4_t(sV + code_off<D>(tok, c + (mi >> 1)), r[0], r[1], r[2], r[3]);
+    for (int t = 0; t < T; ++t) {
+        const int nvalid = tile[t].nvalid;
+        const bool tail = nvalid < DEC_TILE;
+        const int t_lo = 2 * q4, t_hi = 8 + 2 * q4;  // tokens of this lane's A halves
+        const uint32_t mlo = (t_lo < nvalid ? 0x0000ffffu : 0u) | (t_lo + 1 < nvalid ? 0xffff0000u : 0u);
+        const uint32_t mhi = (t_hi < nvalid ? 0x0000ffffu : 0u) | (t_hi + 1 < nvalid ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            uint32_t lo = r[2 * u], hi = r[2 * u + 1];
-            if (tail) {
-                lo &= mlo;
-                hi &= mhi;
-            }
-            uint32_t a0, a1, a2, a3;
-            codes_to_half<FMT, true>(lo, a0, a1);
-            codes_to_half<FMT, true>(hi, a2, a3);
+        for (int c = 0; c < MT; c += 2) {
+            uint32_t r[4];
+            ldsm_x4_t(tile[t].v + code_off<D>(tok, c + (mi >> 1)), r[0], r[1], r[2], r[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16_16816(d, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+            for (int u = 0; u < 2; ++u) {
+                uint32_t lo = r[2 * u], hi = r[2 * u + 1];
+                if (tail) {
+                    lo &= mlo;
+                    hi &= mhi;
+                }
+                uint32_t a0, a1, a2, a3;
+                codes_to_half<FMT, true>(lo, a0, a1);
+                codes_to_half<FMT, true>(hi, a2, a3);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][c + u][e] = fmaf(vs, d[e], acc[nt][c + u][e] * alpha[nt][e & 1]);
+                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][c + u], a0, a1, a2, a3, pb[t][nt][0], pb[t][nt][1]);
             }
         }
     }
@@ -179,13 +229,14 @@ __device__ __forceinline__ void attend_codes(uint32_t sK, uint32_t sV, int nvali
 
 // LATE: the split has late pieces (see k_decode.cu).
 template <int D, int NT, int FMT, bool LATE>
-__global__ void __launch_bounds__(DEC_WARPS * 32, 1)
+__global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     k_decode_quant(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const DecodeArgs a, const float *__restrict__ k_scale, const float *__restrict__ v_scale) {
     constexpr int TILE_BYTES = DEC_TILE * D;
     constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K tile + V tile
     constexpr int MT = D / 16;
     constexpr int HALVES = D / 64;
+    constexpr int WARPS = quant_warps(NT * 8), DQ_STAGES = dq_stages(WARPS);
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -193,10 +244,11 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g4 = lane >> 2, q4 = lane & 3;
     const uint32_t stage0 = base + (uint32_t)(warp * DQ_STAGES) * STAGE_BYTES;
-    const uint32_t bar0 = base + (uint32_t)(DEC_WARPS * DQ_STAGES) * STAGE_BYTES + (uint32_t)(warp * DQ_STAGES) * 8u;
-    QuantMeta *meta = reinterpret_cast<QuantMeta *>(smem_raw + (base - raw) + DEC_WARPS * DQ_STAGES * STAGE_BYTES +
-                                                    DEC_WARPS * DQ_STAGES * 8) +
-                      warp * DQ_STAGES;
+    const uint32_t bar0 = base + (uint32_t)(WARPS * DQ_STAGES) * STAGE_BYTES + (uint32_t)(warp * DQ_STAGES) * 8u;
+    QuantMeta *meta = reinterpret_cast<QuantMeta *>(smem_raw + (base - raw) + WARPS * DQ_STAGES * STAGE_BYTES +
+                                                    WARPS * DQ_STAGES * 8);
+    int32_t *pieces = reinterpret_cast<int32_t *>(meta + WARPS * DQ_STAGES) + warp * DQ_STAGES;  // of the stages' tiles
+    meta += warp * DQ_STAGES;
 
     if (lane == 0) {
         for (int s = 0; s < DQ_STAGES; ++s) mbar_init(bar0 + 8u * s, 1);
@@ -206,13 +258,14 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     }
     __syncwarp();
 
-    const int64_t wid = (int64_t)blockIdx.x * DEC_WARPS + warp;
+    const int64_t wid = (int64_t)blockIdx.x * WARPS + warp;
     if (wid >= a.static_chunks) return;
 
     uint32_t qf[NT][MT][2];
     float hs[NT][2];
     float acc[NT][MT][4];
     float m_run[NT][2], l_run[NT][2];
+    float v_ref = DQ_VMIN, v_inv = 1.f / DQ_VMIN;
 
     // partial of row `r` (at least one tile attended) for piece `c`: slot r + c
     auto write_partial = [&](int64_t r, int64_t c) {
@@ -230,7 +283,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
                     float *o = a.o_part + (slot * a.G + head) * D + 2 * g4;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i], acc[nt][mt][2 + i]);
+                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * v_ref, acc[nt][mt][2 + i] * v_ref);
                     if (g4 == 0) {
                         float *ml = a.ml_part + (slot * a.G + head) * 2;
                         ml[0] = m_run[nt][i] - DQ_PSHIFT;  // what the weights are relative to
@@ -240,6 +293,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
             }
     };
     auto start_row = [&](int64_t r) {
+        v_ref = DQ_VMIN;
+        v_inv = 1.f / DQ_VMIN;
         const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
         const __nv_bfloat16 *qb = a.q + ((size_t)b * a.Hq + (size_t)h * a.G) * D;
 #pragma unroll
@@ -365,22 +420,37 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
                 mbar_arrive_expect_tx(bar, STAGE_BYTES);
                 tma_load_3d(dst, &tmK, 0, rs.y, rs.z, bar);
                 tma_load_3d(dst + TILE_BYTES, &tmV, 0, rs.y, rs.z, bar);
-                meta[st].row = rs.row;
-                meta[st].nvalid = rs.nvalid;
-                meta[st].piece = static_cast<int32_t>(fc);
-                meta[st].ks = ks;
-                meta[st].vs = vs;
+                meta[st] = {rs.row, rs.nvalid, ks, vs};
+                if constexpr (LATE) pieces[st] = static_cast<int32_t>(fc);
             }
             __syncwarp();
             ++issued;
         }
-        // next tile, or the end (row -1)
+        // next tile, or the end (row -1); with the one after it, when that is of the same row and piece
         int64_t row = -1, pc = -1;
-        int nvalid = 0, st = 0;
-        float tks = 0.f, tvs = 0.f;
+        int count = 1;
+        Tile tile[2];
+        auto take = [&](int k, const QuantMeta &m, int st) {
+            const uint32_t at = stage0 + (uint32_t)st * STAGE_BYTES;
+            tile[k] = {at, at + TILE_BYTES, m.nvalid, m.ks, m.vs};
+        };
         if (!failed && consumed != issued) {
-            st = static_cast<int>(consumed % DQ_STAGES);
-            if (!__all_sync(FULL, mbar_wait_sleep(bar0 + 8u * st, (consumed / DQ_STAGES) & 1u))) {
+            const int st = static_cast<int>(consumed % DQ_STAGES), st1 = static_cast<int>((consumed + 1) % DQ_STAGES);
+            const QuantMeta m = meta[st];
+            row = m.row;
+            pc = wid;
+            if constexpr (LATE) pc = pieces[st];
+            take(0, m, st);
+            bool landed = mbar_wait_sleep(bar0 + 8u * st, (consumed / DQ_STAGES) & 1u);
+            if (consumed + 1 != issued) {
+                const QuantMeta m1 = meta[st1];
+                if (m1.row == row && (!LATE || pieces[st1] == pc)) {
+                    count = 2;
+                    take(1, m1, st1);
+                    landed &= mbar_wait_sleep(bar0 + 8u * st1, ((consumed + 1) / DQ_STAGES) & 1u);
+                }
+            }
+            if (!__all_sync(FULL, landed)) {
                 // a load did not arrive in time: report, let every issued load land, drop the
                 // partial in progress (its slot keeps its empty partial) and give every piece
                 // this warp would still have taken its empty partials
@@ -389,17 +459,12 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
                     (void)mbar_wait_bounded(bar0 + 8u * (i % DQ_STAGES), (i / DQ_STAGES) & 1u);
                 failed = true;
                 attended = false;
+                row = -1;
                 while (!fill_done) {
                     const int64_t c = next_piece();
                     if (c >= a.chunks) fill_done = true;
                     else empty_piece(c);
                 }
-            } else {
-                row = meta[st].row;
-                pc = meta[st].piece;
-                nvalid = meta[st].nvalid;
-                tks = meta[st].ks;
-                tvs = meta[st].vs;
             }
         }
         if (row != cur_row || pc != cur_pc) {
@@ -409,24 +474,29 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
             cur_row = row;
             cur_pc = pc;
         }
-        const uint32_t sK = stage0 + (uint32_t)st * STAGE_BYTES;
-        attend_codes<D, NT, FMT>(sK, sK + TILE_BYTES, nvalid, tks, tvs, qf, hs, acc, m_run, l_run, lane);
+        if (count == 2) {
+            attend_codes<D, NT, FMT, 2>(tile, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+        } else {
+            const Tile one[1] = {tile[0]};
+            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+        }
         attended = true;
-        __syncwarp();  // every lane is done with this stage before it is refilled
-        ++consumed;
+        __syncwarp();  // every lane is done with these stages before they are refilled
+        consumed += count;
     }
 }
 
 template <int D, int NT, int FMT>
 cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK, const CUtensorMap &tmV,
                        int grid, cudaStream_t s, bool pdl) {
-    const size_t smem = 1024 + (size_t)DEC_WARPS * DQ_STAGES * (2 * DEC_TILE * D + 8 + sizeof(QuantMeta));
+    constexpr int WARPS = quant_warps(NT * 8);
+    const size_t smem = 1024 + (size_t)WARPS * dq_stages(WARPS) * (2 * DEC_TILE * D + 8 + sizeof(QuantMeta) + sizeof(int32_t));
     const bool late = a.chunks > a.static_chunks;
     auto kern = late ? k_decode_quant<D, NT, FMT, true> : k_decode_quant<D, NT, FMT, false>;
     static std::atomic<unsigned long long> done[2];
     cudaError_t e = ensure_smem_limit(kern, (int)smem, done[late ? 1 : 0]);
     if (e != cudaSuccess) return e;
-    return launch_k(kern, dim3(grid), dim3(DEC_WARPS * 32), smem, s, pdl, tmK, tmV, a, (const float *)qa.k_scale,
+    return launch_k(kern, dim3(grid), dim3(WARPS * 32), smem, s, pdl, tmK, tmV, a, (const float *)qa.k_scale,
                     (const float *)qa.v_scale);
 }
 

@@ -137,7 +137,8 @@ struct Plan {
 };
 
 
-vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
+// warps: worker warps of a GQA decode block
+vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p, int warps = vx::DEC_WARPS) {
     p->mla = g->mla_shared_kv != 0;
     p->G = g->num_q_heads / g->num_kv_heads;
     p->rows = (int64_t)g->batch * g->num_kv_heads;
@@ -149,7 +150,7 @@ vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
     if (planned) {
         int sms = 0;
         if (sm_count_current(&sms) != 0) return fail(VX_ERR_CUDA, "cannot query the current device's SM count");
-        w = p->mla ? (int64_t)sms : (int64_t)sms * vx::DEC_WARPS;  // MLA: one CTA per SM
+        w = p->mla ? (int64_t)sms : (int64_t)sms * warps;  // MLA: one CTA per SM
     }
     if (w > p->units) w = p->units;
     if (w < 1) w = 1;
@@ -181,7 +182,7 @@ vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
     p->static_units = us;
     p->static_chunks = static_cast<int32_t>(ws_);
     p->chunks = static_cast<int32_t>(ws_ + wd);
-    p->grid = p->mla ? p->chunks : (p->static_chunks + vx::DEC_WARPS - 1) / vx::DEC_WARPS;
+    p->grid = p->mla ? p->chunks : (p->static_chunks + warps - 1) / warps;
     return VX_OK;
 }
 
@@ -261,6 +262,11 @@ WsLayout ws_layout(const vx_geometry *g, int32_t max_pages, int32_t k, const Pla
 
 // bytes vx_sparse_decode uses: the split partials (the start of the layout)
 size_t decode_ws_bytes(const WsLayout &l) { return l.scores; }
+
+// the 8-bit decode's plan: the same split rule for its own count of warps
+vx_status plan_quant(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
+    return plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads));
+}
 
 // ------------------------------------------------------------------ TMA descriptors
 
@@ -601,7 +607,12 @@ size_t vx_workspace_size(const vx_geometry *geo, int32_t max_pages, int32_t k, i
     }
     Plan p;
     if (plan(geo, k, num_splits, &p) != VX_OK) return 0;
-    return ws_layout(geo, max_pages, k, p).total;
+    size_t n = ws_layout(geo, max_pages, k, p).total;
+    if (!geo->mla_shared_kv) {  // enough for the 8-bit calls too
+        if (plan_quant(geo, k, num_splits, &p) != VX_OK) return 0;
+        n = std::max(n, ws_layout(geo, max_pages, k, p).total);
+    }
+    return n;
 }
 
 int32_t vx_planned_splits(const vx_geometry *geo, int32_t max_pages, int32_t k) {
@@ -682,7 +693,7 @@ vx_status sparse_decode(const vx_geometry *geo, const vx_page_table *table, cons
     if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
     if (!std::isfinite(sm_scale)) return fail(VX_ERR_INVALID_ARG, "sm_scale must be finite");
     Plan p;
-    VX_TRY(plan(geo, k, num_splits, &p));
+    VX_TRY(quant ? plan_quant(geo, k, num_splits, &p) : plan(geo, k, num_splits, &p));
     const WsLayout l = ws_layout(geo, table->max_pages, k, p);
     if (!ws || !al16(ws)) return fail(VX_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
     if (ws_bytes < decode_ws_bytes(l))
@@ -725,7 +736,7 @@ vx_status fused_step(const vx_geometry *geo, const vx_page_table *table, const v
     if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
     if (!std::isfinite(sm_scale)) return fail(VX_ERR_INVALID_ARG, "sm_scale must be finite");
     Plan p;
-    VX_TRY(plan(geo, k, num_splits, &p));
+    VX_TRY(quant ? plan_quant(geo, k, num_splits, &p) : plan(geo, k, num_splits, &p));
     const WsLayout l = ws_layout(geo, table->max_pages, k, p);
     if (!ws || !al16(ws)) return fail(VX_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
     if (ws_bytes < l.total)

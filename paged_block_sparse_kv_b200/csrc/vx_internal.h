@@ -29,6 +29,8 @@ constexpr int DEC_TILE = 16;             // GQA decode: tokens per tile (one mma
 constexpr int DEC_DYN_PCT = 25;          // GQA decode, planned split: % of tiles handed out late
 constexpr int DEC_DYN_DIV = 8;           // ... in pieces of 1 / DEC_DYN_DIV of a warp's share of tiles
 constexpr int DEC_DYN_MIN_PIECE = 8;     // ... only when such a piece has at least this many tiles
+constexpr int DQ_WARPS = 16;             // 8-bit decode, up to 8 query heads per KV head: warps per block
+constexpr int DQ_WARPS_WIDE = 8;         // ... more query heads (twice the registers)
 constexpr int MLA_MIN_PAGE = 32;         // MLA decode: pages of 32 or 64 tokens
 constexpr int MLA_TILE_ROWS = 64;        // MLA decode: tokens per tile (a page of up to 64 tokens)
 
@@ -261,6 +263,8 @@ cudaError_t ensure_smem_limit(F kern, int bytes, std::atomic<unsigned long long>
     return e;
 }
 
+// warps per block of the 8-bit decode for groups of G query heads
+__host__ __device__ constexpr int quant_warps(int G) { return G <= 8 ? DQ_WARPS : DQ_WARPS_WIDE; }
 // chunk c of W covers units [c*T/W, (c+1)*T/W)
 __host__ __device__ __forceinline__ int64_t chunk_start(int64_t c, int64_t T, int64_t W) {
     return (c * T) / W;
