@@ -82,6 +82,14 @@ __device__ __forceinline__ uint32_t code_off(int row, int chunk) {
     return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
+// 4 bytes global -> shared, asynchronously; cp_async_arrive: one arrival on `bar` once the thread's
+// copies so far have landed
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -251,7 +259,8 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     meta += warp * DQ_STAGES;
 
     if (lane == 0) {
-        for (int s = 0; s < DQ_STAGES; ++s) mbar_init(bar0 + 8u * s, 1);
+        // two arrivals complete a stage: the one that announces its bytes, and its scales' copies
+        for (int s = 0; s < DQ_STAGES; ++s) mbar_init(bar0 + 8u * s, 2);
         fence_mbar_init();
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
@@ -367,32 +376,24 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     };
 
     int64_t fc = wid, batch = p_start(wid), f_end = p_start(wid + 1);
-    int64_t cur_row = batch / a.units_per_row, cur_pc = wid;  // (row, piece) being accumulated
-    bool attended = false;                                    // it has a tile
-    // the query is an input of the call, complete before this grid starts, and the workspace is
-    // not touched by the previous kernel: only the selection waits for it
-    start_row(cur_row);
-    empty_piece(fc);
+    int64_t cur_row = -1, cur_pc = -1;  // (row, piece) being accumulated
+    bool attended = false;              // it has a tile
+    // nothing is read before the wait: the first row's query is loaded and scaled while its first
+    // tiles are on their way
     pdl_wait();
 
     Resolved rs;
-    float ks, vs;
     auto resolve = [&]() {
         rs = resolve_unit(a, batch + lane, f_end);
-        ks = vs = 0.f;
-        if (rs.valid) {
-            ks = __ldg(k_scale + rs.z);
-            vs = __ldg(v_scale + rs.z);
-        }
         return __ballot_sync(FULL, rs.valid);
     };
     uint32_t pending = resolve();
     uint32_t issued = 0, consumed = 0;
-    bool fill_done = false, failed = false;
+    bool fill_done = false, started = false;
 
     for (;;) {
         // issue loads until the ring is full or no piece is left
-        while (!failed && !fill_done && issued - consumed < DQ_STAGES) {
+        while (!fill_done && issued - consumed < DQ_STAGES) {
             if (pending == 0) {
                 batch += 32;
                 if (batch >= f_end) {
@@ -420,60 +421,62 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
                 mbar_arrive_expect_tx(bar, STAGE_BYTES);
                 tma_load_3d(dst, &tmK, 0, rs.y, rs.z, bar);
                 tma_load_3d(dst + TILE_BYTES, &tmV, 0, rs.y, rs.z, bar);
-                meta[st] = {rs.row, rs.nvalid, ks, vs};
+                // the page's scales straight into the stage's metadata: no thread waits for them
+                cp_async_4(smem_u32(&meta[st].ks), k_scale + rs.z);
+                cp_async_4(smem_u32(&meta[st].vs), v_scale + rs.z);
+                cp_async_arrive(bar);
+                *reinterpret_cast<int2 *>(&meta[st]) = make_int2(rs.row, rs.nvalid);
                 if constexpr (LATE) pieces[st] = static_cast<int32_t>(fc);
             }
             __syncwarp();
             ++issued;
         }
+        if (!started) {
+            empty_piece(wid);
+            started = true;
+        }
         // next tile, or the end (row -1); with the one after it, when that is of the same row and piece
         int64_t row = -1, pc = -1;
         int count = 1;
-        Tile tile[2];
-        auto take = [&](int k, const QuantMeta &m, int st) {
-            const uint32_t at = stage0 + (uint32_t)st * STAGE_BYTES;
-            tile[k] = {at, at + TILE_BYTES, m.nvalid, m.ks, m.vs};
-        };
-        if (!failed && consumed != issued) {
-            const int st = static_cast<int>(consumed % DQ_STAGES), st1 = static_cast<int>((consumed + 1) % DQ_STAGES);
-            const QuantMeta m = meta[st];
-            row = m.row;
+        const int st = static_cast<int>(consumed % DQ_STAGES), st1 = static_cast<int>((consumed + 1) % DQ_STAGES);
+        if (consumed != issued) {
+            row = meta[st].row;
             pc = wid;
             if constexpr (LATE) pc = pieces[st];
-            take(0, m, st);
-            bool landed = mbar_wait_sleep(bar0 + 8u * st, (consumed / DQ_STAGES) & 1u);
-            if (consumed + 1 != issued) {
-                const QuantMeta m1 = meta[st1];
-                if (m1.row == row && (!LATE || pieces[st1] == pc)) {
-                    count = 2;
-                    take(1, m1, st1);
-                    landed &= mbar_wait_sleep(bar0 + 8u * st1, ((consumed + 1) / DQ_STAGES) & 1u);
-                }
-            }
-            if (!__all_sync(FULL, landed)) {
-                // a load did not arrive in time: report, let every issued load land, drop the
-                // partial in progress (its slot keeps its empty partial) and give every piece
-                // this warp would still have taken its empty partials
-                if (lane == 0) set_err(a.err, VX_DATA_TIMEOUT);
-                for (uint32_t i = consumed; i < issued; ++i)
-                    (void)mbar_wait_bounded(bar0 + 8u * (i % DQ_STAGES), (i / DQ_STAGES) & 1u);
-                failed = true;
-                attended = false;
-                row = -1;
-                while (!fill_done) {
-                    const int64_t c = next_piece();
-                    if (c >= a.chunks) fill_done = true;
-                    else empty_piece(c);
-                }
-            }
+            if (consumed + 1 != issued && meta[st1].row == row && (!LATE || pieces[st1] == pc)) count = 2;
         }
-        if (row != cur_row || pc != cur_pc) {
+        if (row < 0 || row != cur_row || pc != cur_pc) {
             if (attended) write_partial(cur_row, cur_pc);
-            if (row < 0) break;
+            if (row < 0) break;  // also of a warp that had no tile at all
             if (row != cur_row || attended) start_row(row);
+            attended = false;
             cur_row = row;
             cur_pc = pc;
         }
+        bool landed = mbar_wait_sleep(bar0 + 8u * st, (consumed / DQ_STAGES) & 1u);
+        if (count == 2) landed &= mbar_wait_sleep(bar0 + 8u * st1, ((consumed + 1) / DQ_STAGES) & 1u);
+        if (!__all_sync(FULL, landed)) {
+            // a load did not arrive in time: report, let every issued load land, drop the partial in
+            // progress (its slot keeps its empty partial) and give every piece this warp would
+            // still have taken its empty partials
+            if (lane == 0) set_err(a.err, VX_DATA_TIMEOUT);
+            for (uint32_t i = consumed; i < issued; ++i)
+                (void)mbar_wait_bounded(bar0 + 8u * (i % DQ_STAGES), (i / DQ_STAGES) & 1u);
+            while (!fill_done) {
+                const int64_t c = next_piece();
+                if (c >= a.chunks) fill_done = true;
+                else empty_piece(c);
+            }
+            break;
+        }
+        Tile tile[2];
+        auto take = [&](int k, int s) {
+            const QuantMeta m = meta[s];
+            const uint32_t at = stage0 + (uint32_t)s * STAGE_BYTES;
+            tile[k] = {at, at + TILE_BYTES, m.nvalid, m.ks, m.vs};
+        };
+        take(0, st);
+        if (count == 2) take(1, st1);
         if (count == 2) {
             attend_codes<D, NT, FMT, 2>(tile, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
         } else {

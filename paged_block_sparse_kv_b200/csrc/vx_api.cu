@@ -414,7 +414,8 @@ vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q,
         CUtensorMap tmK, tmV;
         VX_TRY(make_code_map(&tmK, quant->k_cache, g->head_dim_qk, g->page_size, page_heads));
         VX_TRY(make_code_map(&tmV, quant->v_cache, g->head_dim_v, g->page_size, page_heads));
-        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.grid, s, pdl);
+        // (always with a programmatic launch: the kernel reads nothing before its dependency wait)
+        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.grid, s, true);
     } else if (p.mla) {
         CUtensorMap tmK, tmQ;
         VX_TRY(make_cache_map_blocks(&tmK, k_cache, g->head_dim_qk, g->page_size, page_heads,
