@@ -235,6 +235,44 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
     }
 }
 
+// The group's query heads (row-major from qb, G of them) as mma B fragments in the dims order above,
+// each scaled into fp16's range, and the logits' scale (log2 units) that undoes it.
+template <int D, int NT>
+__device__ __forceinline__ void load_query(const __nv_bfloat16 *qb, int G, float scale_log2, uint32_t (&qf)[NT][D / 16][2],
+                                           float (&hs)[NT][2], int lane) {
+    constexpr int MT = D / 16, HALVES = D / 64;
+    const int g4 = lane >> 2, q4 = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int head = nt * 8 + g4;
+        uint2 w[MT];  // dims (HALVES q4 + half) 16 + 4 st .. + 3 of step half * 4 + st
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            w[i] = make_uint2(0u, 0u);
+            if (head < G)
+                w[i] = *reinterpret_cast<const uint2 *>(qb + (size_t)head * D + (HALVES * q4 + i / 4) * 16 + (i & 3) * 4);
+            top = __vmaxu2(top, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+        }
+        uint32_t amax = max(top & 0xffffu, top >> 16);
+        amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
+        amax = max(amax, __shfl_xor_sync(FULL, amax, 2));
+        // 2^(14 - exponent of the largest element), kept in fp32's normal range
+        const uint32_t ef = min(268u - (amax >> 7), 253u);
+        const float mul = __uint_as_float(ef << 23);
+        const float inv = __uint_as_float((254u - ef) << 23) * scale_log2;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            qf[nt][i][0] = half2_bits(__floats2half2_rn(__uint_as_float(w[i].x << 16) * mul,
+                                                        __uint_as_float(w[i].x & 0xffff0000u) * mul));
+            qf[nt][i][1] = half2_bits(__floats2half2_rn(__uint_as_float(w[i].y << 16) * mul,
+                                                        __uint_as_float(w[i].y & 0xffff0000u) * mul));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) hs[nt][i] = __shfl_sync(FULL, inv, (2 * q4 + i) * 4);
+    }
+}
+
 // LATE: the split has late pieces (see k_decode.cu).
 template <int D, int NT, int FMT, bool LATE>
 __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
@@ -243,7 +281,6 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     constexpr int TILE_BYTES = DEC_TILE * D;
     constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K tile + V tile
     constexpr int MT = D / 16;
-    constexpr int HALVES = D / 64;
     constexpr int WARPS = quant_warps(NT * 8), DQ_STAGES = dq_stages(WARPS);
 
     extern __shared__ uint8_t smem_raw[];
@@ -306,35 +343,11 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
         v_inv = 1.f / DQ_VMIN;
         const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
         const __nv_bfloat16 *qb = a.q + ((size_t)b * a.Hq + (size_t)h * a.G) * D;
+        load_query<D, NT>(qb, a.G, a.scale_log2, qf, hs, lane);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int head = nt * 8 + g4;
-            uint2 w[MT];  // dims (HALVES q4 + half) 16 + 4 st .. + 3 of step half * 4 + st
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                w[i] = make_uint2(0u, 0u);
-                if (head < a.G)
-                    w[i] = *reinterpret_cast<const uint2 *>(qb + (size_t)head * D + (HALVES * q4 + i / 4) * 16 + (i & 3) * 4);
-                top = __vmaxu2(top, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
-            }
-            uint32_t amax = max(top & 0xffffu, top >> 16);
-            amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
-            amax = max(amax, __shfl_xor_sync(FULL, amax, 2));
-            // 2^(14 - exponent of the largest element), kept in fp32's normal range
-            const uint32_t ef = min(268u - (amax >> 7), 253u);
-            const float mul = __uint_as_float(ef << 23);
-            const float inv = __uint_as_float((254u - ef) << 23) * a.scale_log2;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                qf[nt][i][0] = half2_bits(__floats2half2_rn(__uint_as_float(w[i].x << 16) * mul,
-                                                            __uint_as_float(w[i].x & 0xffff0000u) * mul));
-                qf[nt][i][1] = half2_bits(__floats2half2_rn(__uint_as_float(w[i].y << 16) * mul,
-                                                            __uint_as_float(w[i].y & 0xffff0000u) * mul));
-            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                hs[nt][i] = __shfl_sync(FULL, inv, (2 * q4 + i) * 4);
                 m_run[nt][i] = -INFINITY;
                 l_run[nt][i] = 0.f;
             }
@@ -489,11 +502,155 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     }
 }
 
+// One block per (request, KV head) row of at most DQ_ROW_TILES tiles: warp w attends tiles 2 w and
+// 2 w + 1 (and 2 (w + WARPS), ...), and the warps' partials meet in shared memory, in warp order:
+// no partial goes through memory and no merge kernel follows.
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
+    k_decode_quant_row(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const DecodeArgs a, const float *__restrict__ k_scale, const float *__restrict__ v_scale) {
+    constexpr int WARPS = quant_warps(NT * 8), SLOTS = DQ_ROW_TILES / WARPS;  // tiles of a warp, loaded at once
+    constexpr int TILE_BYTES = DEC_TILE * D, MT = D / 16;
+    static_assert(SLOTS % 2 == 0, "tiles go in pairs");
+    __shared__ uint64_t s_bar[WARPS];
+    __shared__ float s_ml[WARPS][NT * 8][2];
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    float *s_o = reinterpret_cast<float *>(smem_raw + (base - raw));  // [warp][head][dim], after the tiles
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g4 = lane >> 2, q4 = lane & 3;
+    const uint32_t bar = smem_u32(&s_bar[warp]);
+    if (lane == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    __syncwarp();
+    pdl_wait();
+    pdl_trigger();  // this grid's dependent waits for its end; it may land now
+    const int64_t r = blockIdx.x;
+    // lane s < SLOTS: this warp's tile s, which is tile (s / 2 * WARPS + warp) * 2 + s % 2 of the row
+    const int64_t u = (int64_t)((lane >> 1) * WARPS + warp) * 2 + (lane & 1);
+    Resolved rs{0, 0, 0, 0, false};
+    if (lane < SLOTS && u < a.units_per_row)
+        rs = resolve_unit(a, r * a.units_per_row + u, (r + 1) * a.units_per_row);
+    const uint32_t valid = __ballot_sync(FULL, rs.valid);
+    float ks = 0.f, vs = 0.f;
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(valid) * 2 * TILE_BYTES);
+    __syncwarp();
+    const uint32_t tiles = base + (uint32_t)(warp * SLOTS) * 2 * TILE_BYTES;
+    if (rs.valid) {
+        const uint32_t dst = tiles + (uint32_t)lane * 2 * TILE_BYTES;
+        tma_load_3d(dst, &tmK, 0, rs.y, rs.z, bar);
+        tma_load_3d(dst + TILE_BYTES, &tmV, 0, rs.y, rs.z, bar);
+        ks = __ldg(k_scale + rs.z);
+        vs = __ldg(v_scale + rs.z);
+    }
+    const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
+    uint32_t qf[NT][MT][2];
+    float hs[NT][2], acc[NT][MT][4], m_run[NT][2], l_run[NT][2];
+    float v_ref = DQ_VMIN, v_inv = 1.f / DQ_VMIN;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m_run[nt][i] = -INFINITY;
+            l_run[nt][i] = 0.f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
+    }
+    bool landed = true;
+    if (valid) {
+        load_query<D, NT>(a.q + ((size_t)b * a.Hq + (size_t)h * a.G) * D, a.G, a.scale_log2, qf, hs, lane);
+        landed = __all_sync(FULL, mbar_wait_bounded(bar, 0));
+        if (!landed) {  // report, and let the loads land before shared memory is used for the partials
+            if (lane == 0) set_err(a.err, VX_DATA_TIMEOUT);
+            (void)mbar_wait_bounded(bar, 0);
+        }
+    }
+    uint32_t left = landed ? valid : 0u;
+    auto next_tile = [&]() -> Tile {  // the lowest of `left`
+        const int s = __ffs(left) - 1;
+        left &= left - 1;
+        const uint32_t at = tiles + (uint32_t)s * 2 * TILE_BYTES;
+        return {at, at + TILE_BYTES, __shfl_sync(FULL, rs.nvalid, s), __shfl_sync(FULL, ks, s), __shfl_sync(FULL, vs, s)};
+    };
+#pragma unroll 1
+    while (left) {
+        const Tile t0 = next_tile();
+        if (left) {
+            const Tile pair[2] = {t0, next_tile()};
+            attend_codes<D, NT, FMT, 2>(pair, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+        } else {
+            const Tile one[1] = {t0};
+            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+        }
+    }
+    __syncthreads();  // every warp is done with its tiles (after a timeout: with its bounded wait)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int head = nt * 8 + 2 * q4 + i;
+            float v = l_run[nt][i];
+            v += __shfl_xor_sync(FULL, v, 4);
+            v += __shfl_xor_sync(FULL, v, 8);
+            v += __shfl_xor_sync(FULL, v, 16);
+            if (g4 == 0) {
+                s_ml[warp][head][0] = m_run[nt][i];
+                s_ml[warp][head][1] = v;
+            }
+            if (head < a.G && valid) {
+                float *o = s_o + (warp * a.G + head) * D + 2 * g4;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * v_ref, acc[nt][mt][2 + i] * v_ref);
+            }
+        }
+    __syncthreads();
+    // two dims per thread; a warp without a tile has the maximum -inf and left no output
+    for (int e = threadIdx.x; e < a.G * (D / 2); e += WARPS * 32) {
+        const int head = e / (D / 2), dim = (e % (D / 2)) * 2;
+        float M = -INFINITY, l = 0.f;
+        float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][head][0]);
+#pragma unroll 4
+        for (int w = 0; w < WARPS; ++w) {
+            const float m = s_ml[w][head][0];
+            if (m == -INFINITY) continue;
+            const float f = exp2f(m - M);
+            const float2 x = *reinterpret_cast<const float2 *>(s_o + (w * a.G + head) * D + dim);
+            l += f * s_ml[w][head][1];
+            o.x += f * x.x;
+            o.y += f * x.y;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const size_t at = (size_t)b * a.Hq + (size_t)h * a.G + head;
+        *reinterpret_cast<uint32_t *>(a.out + at * D + dim) = pack_bf16x2(o.x * inv, o.y * inv);
+        // the weights were relative to 2^-DQ_PSHIFT of the maximum
+        if (a.lse && dim == 0) a.lse[at] = l > 0.f ? (M - DQ_PSHIFT + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
 template <int D, int NT, int FMT>
 cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK, const CUtensorMap &tmV,
                        int grid, cudaStream_t s, bool pdl) {
     constexpr int WARPS = quant_warps(NT * 8);
     const size_t smem = 1024 + (size_t)WARPS * dq_stages(WARPS) * (2 * DEC_TILE * D + 8 + sizeof(QuantMeta) + sizeof(int32_t));
+    if (a.chunks == 0) {  // a block per row
+        constexpr size_t tiles = (size_t)DQ_ROW_TILES * 2 * DEC_TILE * D, parts = (size_t)WARPS * NT * 8 * D * 4;
+        const size_t row_smem = 1024 + (tiles > parts ? tiles : parts);
+        static std::atomic<unsigned long long> row_done;
+        cudaError_t e = ensure_smem_limit(k_decode_quant_row<D, NT, FMT>, (int)row_smem, row_done);
+        if (e != cudaSuccess) return e;
+        return launch_k(k_decode_quant_row<D, NT, FMT>, dim3(grid), dim3(WARPS * 32), row_smem, s, pdl, tmK, tmV, a,
+                        (const float *)qa.k_scale, (const float *)qa.v_scale);
+    }
     const bool late = a.chunks > a.static_chunks;
     auto kern = late ? k_decode_quant<D, NT, FMT, true> : k_decode_quant<D, NT, FMT, false>;
     static std::atomic<unsigned long long> done[2];

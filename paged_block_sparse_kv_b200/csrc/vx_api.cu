@@ -134,6 +134,7 @@ struct Plan {
     int32_t tiles_per_page, chunks, static_chunks, grid;
     int G;
     bool mla;
+    bool by_row = false;  // 8-bit decode: one block per row, no split (see plan_quant)
 };
 
 
@@ -264,8 +265,16 @@ WsLayout ws_layout(const vx_geometry *g, int32_t max_pages, int32_t k, const Pla
 size_t decode_ws_bytes(const WsLayout &l) { return l.scores; }
 
 // the 8-bit decode's plan: the same split rule for its own count of warps
+// Planned, and with no more rows than SMs and short rows: a block per row, whose warps join their
+// partials in shared memory, instead of a split over the GPU and the merge kernel.  Measured, split
+// and row (us): 8 rows of 8 tiles 8.6 and 4.7, 128 rows of 32 tiles 11.4 and 8.3; with more rows than
+// SMs the second wave costs more: 256 rows of 32 tiles 15.6 and 16.2, 512 rows of 8 tiles 11.9 and
+// 18.7.
 vx_status plan_quant(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
-    return plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads));
+    VX_TRY(plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads)));
+    int sms = 0;
+    p->by_row = num_splits <= 0 && p->units_per_row <= vx::DQ_ROW_TILES && sm_count_current(&sms) == 0 && p->rows <= sms;
+    return VX_OK;
 }
 
 // ------------------------------------------------------------------ TMA descriptors
@@ -415,7 +424,9 @@ vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q,
         VX_TRY(make_code_map(&tmK, quant->k_cache, g->head_dim_qk, g->page_size, page_heads));
         VX_TRY(make_code_map(&tmV, quant->v_cache, g->head_dim_v, g->page_size, page_heads));
         // (always with a programmatic launch: the kernel reads nothing before its dependency wait)
-        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.grid, s, true);
+        if (p.by_row) a.chunks = 0;
+        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.by_row ? (int)p.rows : p.grid, s, true);
+        if (p.by_row) return e == cudaSuccess ? VX_OK : cuda_fail(e, "sparse decode launch");
     } else if (p.mla) {
         CUtensorMap tmK, tmQ;
         VX_TRY(make_cache_map_blocks(&tmK, k_cache, g->head_dim_qk, g->page_size, page_heads,

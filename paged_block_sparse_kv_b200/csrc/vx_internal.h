@@ -31,6 +31,7 @@ constexpr int DEC_DYN_DIV = 8;           // ... in pieces of 1 / DEC_DYN_DIV of 
 constexpr int DEC_DYN_MIN_PIECE = 8;     // ... only when such a piece has at least this many tiles
 constexpr int DQ_WARPS = 16;             // 8-bit decode, up to 8 query heads per KV head: warps per block
 constexpr int DQ_WARPS_WIDE = 8;         // ... more query heads (twice the registers)
+constexpr int DQ_ROW_TILES = 32;         // ... rows of at most this many tiles may go to one block each
 constexpr int MLA_MIN_PAGE = 32;         // MLA decode: pages of 32 or 64 tokens
 constexpr int MLA_TILE_ROWS = 64;        // MLA decode: tokens per tile (a page of up to 64 tokens)
 
@@ -193,7 +194,8 @@ cudaError_t launch_decode_gqa(const DecodeArgs &a, const CUtensorMap &tmK, const
 // grid = split count (one CTA per split); tmQ views q as (64 columns, rows = batch * Hq, 9 blocks)
 cudaError_t launch_decode_mla(const DecodeArgs &a, const CUtensorMap &tmK, const CUtensorMap &tmQ, int grid,
                               cudaStream_t s, bool pdl);
-// grid: blocks of DEC_WARPS warps; tmK and tmV view the codes as (head_dim, page_size, page-heads)
+// grid: blocks of quant_warps(G) warps; a.chunks == 0: one block per row, which writes out and lse
+// itself (no merge).  tmK and tmV view the codes as (head_dim, page_size, page-heads)
 cudaError_t launch_decode_quant(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK,
                                 const CUtensorMap &tmV, int grid, cudaStream_t s, bool pdl);
 // a.k_cache, a.v_cache unused; mode CEN_APPEND or CEN_PREFILL
