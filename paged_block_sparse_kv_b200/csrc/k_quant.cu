@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_prefill(const CentroidA
     __shared__ uint32_t s_max[QZ_WARPS];
     __shared__ float s_sum[WPU > 1 ? QZ_WARPS : 1][D];
     __shared__ long long s_part[QZ_WARPS];
+    pdl_wait();
     const int b = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t L = a.seq_lens[b], fp = a.first_pos[b];
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_prefill(const CentroidA
 // a row) of every RPL-th row, and the new row's elements that belong to them.
 template <int D, int NR, int FMT>
 __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_append(const CentroidArgs a, const QuantArgs qa) {
+    pdl_wait();
     // a dependent scorer (vx_block_topk_decode_append_quant) may launch now; it waits for this
     // grid's end and writes before it reads anything
     pdl_trigger();
@@ -540,12 +542,11 @@ template <int D, int P, int FMT>
 cudaError_t launch_qdpf(const CentroidArgs &a, const QuantArgs &qa, int mode, cudaStream_t s) {
     if (mode == CEN_APPEND) {
         const dim3 grid((2 * a.Hkv + QZ_WARPS - 1) / QZ_WARPS, a.B);
-        k_quant_append<D, P * D / 512, FMT><<<grid, QZ_WARPS * 32, 0, s>>>(a, qa);
+        return launch_k(k_quant_append<D, P * D / 512, FMT>, grid, dim3(QZ_WARPS * 32), 0, s, true, a, qa);
     } else {
         const dim3 grid((a.max_pages + QZ_PAGES_PER_BLOCK - 1) / QZ_PAGES_PER_BLOCK, a.B);
-        k_quant_prefill<D, P / 16, FMT><<<grid, QZ_WARPS * 32, 0, s>>>(a, qa);
+        return launch_k(k_quant_prefill<D, P / 16, FMT>, grid, dim3(QZ_WARPS * 32), 0, s, true, a, qa);
     }
-    return cudaGetLastError();
 }
 
 template <int D, int P>
