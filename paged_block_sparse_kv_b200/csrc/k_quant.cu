@@ -75,12 +75,21 @@ __device__ __forceinline__ uint32_t four_codes(float x0, float x1, float x2, flo
     }
 }
 
-// bf16(s * sum / m), rounded once.  A whole page (m a power of two) under a power-of-two scale of
-// ordinary size needs no division: scaling is exact.
-__device__ __forceinline__ uint32_t centroid_bits(float s, float sum, int m) {
-    if ((m & (m - 1)) == 0 && (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-80f && s <= 0x1p80f)
-        return __bfloat16_as_ushort(__float2bfloat16_rn(sum * (s / static_cast<float>(m))));
-    return f64_to_bf16_rne((double)s * sum / m);
+// bf16(s * sum / m), rounded once.  Under a power-of-two scale of ordinary size (`plain`) fp32 will
+// do, as scaling by s is exact: a whole page (m a power of two) needs no division; else the
+// quotient is cut off, its last bit set when a remainder was lost (so that nothing looks like a
+// tie that is none), and rounded to bf16.
+__device__ __forceinline__ bool plain_scale(float s) {
+    return (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-80f && s <= 0x1p80f;
+}
+__device__ __noinline__ uint32_t centroid_f64(float s, float sum, int m) { return f64_to_bf16_rne((double)s * sum / m); }
+__device__ __forceinline__ uint32_t centroid_bits(bool plain, float s, float sum, int m) {
+    if (!plain) return centroid_f64(s, sum, m);
+    if ((m & (m - 1)) == 0) return __bfloat16_as_ushort(__float2bfloat16_rn(sum * (s / static_cast<float>(m))));
+    const float d = static_cast<float>(m), q = __fdiv_rz(sum, d);
+    const uint32_t lost = __fmaf_rn(-q, d, sum) != 0.f ? 1u : 0u;
+    const __nv_bfloat16 c = __float2bfloat16_rn(__uint_as_float(__float_as_uint(q) | lost));
+    return __float_as_uint(__bfloat162float(c) * s) >> 16;
 }
 
 // An infinity becomes the largest finite value of its sign, a NaN zero; returns the new largest
@@ -211,9 +220,11 @@ __device__ __forceinline__ void quant_new_unit(bool go, bool is_key, int part, R
         __syncthreads();  // s_max and s_sum are free again
     }
     if (go && part == 0 && is_key && lane < CPR) {
+        const bool plain = plain_scale(s);
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = centroid_bits(s, sum[2 * e], m) | (centroid_bits(s, sum[2 * e + 1], m) << 16);
+        for (int e = 0; e < 4; ++e)
+            w[e] = centroid_bits(plain, s, sum[2 * e], m) | (centroid_bits(plain, s, sum[2 * e + 1], m) << 16);
         *reinterpret_cast<uint4 *>(cen + chunk * 8) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
@@ -324,9 +335,11 @@ __device__ __forceinline__ void quant_unit(bool go, bool is_key, int part, RowF 
     if (go && part == 0) {
         if (lane == 0) *scale = s;
         if (is_key && lane < CPR) {
+            const bool plain = plain_scale(s);
             uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = centroid_bits(s, sum[2 * e], m) | (centroid_bits(s, sum[2 * e + 1], m) << 16);
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e)
+                w[e] = centroid_bits(plain, s, sum[2 * e], m) | (centroid_bits(plain, s, sum[2 * e + 1], m) << 16);
             *reinterpret_cast<uint4 *>(cen + chunk * 8) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
@@ -532,10 +545,20 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_append(const CentroidAr
             for (int e = 0; e < 16; ++e) sum[e] += __shfl_xor_sync(FULL, sum[e], off);
     }
     // every row lane holds all 16 sums: row lane r writes words r, r + RPL, ... of the chunk's 8
+    // (taken out of the registers first: the arithmetic runs once for all lanes)
     auto *cen = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.centroids) + blk * D + chunk * 16);
+    const bool plain = plain_scale(s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e % RPL == t0) cen[e] = centroid_bits(s, sum[2 * e], slot + 1) | (centroid_bits(s, sum[2 * e + 1], slot + 1) << 16);
+    for (int j = 0; j < 8 / RPL; ++j) {
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int r = 0; r < RPL; ++r)
+            if (r == t0) {
+                x0 = sum[2 * (j * RPL + r)];
+                x1 = sum[2 * (j * RPL + r) + 1];
+            }
+        cen[j * RPL + t0] = centroid_bits(plain, s, x0, slot + 1) | (centroid_bits(plain, s, x1, slot + 1) << 16);
+    }
 }
 
 template <int D, int P, int FMT>
