@@ -229,13 +229,15 @@ __device__ __forceinline__ void quant_new_unit(bool go, bool is_key, int part, R
     }
 }
 
-// One unit of a page with older tokens, by its WPU warps (this warp: rows [16 * part, 16 * part + 16)).  Rows [0, n_old) are
-// the page's older tokens, [n_old, m) come from new_row(t).  `go`: the unit exists (warps of
-// missing units only take part in the block barriers).
-template <int D, int WPU, int FMT, typename RowF>
-__device__ __forceinline__ void quant_unit(bool go, bool is_key, int part, RowF new_row, uint8_t *__restrict__ codes,
-                                           float *__restrict__ scale, __nv_bfloat16 *__restrict__ cen, int n_old,
-                                           int m, int32_t *err, int lane, uint32_t *s_max, float (*s_sum)[D]) {
+// One unit of a page with older tokens, by its WPU warps (this warp: rows [16 * part, 16 * part +
+// 16)).  Rows [0, n_old) are the page's older tokens, row t of [n_old, m) is src + t * stride.
+// `go`: the unit exists (warps of missing units only take part in the block barriers).  At most one
+// page of a chunk: not inlined, so that the usual path keeps its registers.
+template <int D, int WPU, int FMT>
+__device__ __noinline__ void quant_unit(bool go, bool is_key, int part, const __nv_bfloat16 *__restrict__ src,
+                                        int64_t stride, uint8_t *__restrict__ codes, float *__restrict__ scale,
+                                        __nv_bfloat16 *__restrict__ cen, int n_old, int m, int32_t *err, int lane,
+                                        uint32_t *s_max, float (*s_sum)[D]) {
     constexpr int CPR = D / 8;    // 16-byte chunks of a new row = 8-byte chunks of a code row
     constexpr int RPL = 32 / CPR; // rows per warp-wide load
     constexpr int NR = 16 / RPL;  // rows per lane
@@ -249,7 +251,7 @@ __device__ __forceinline__ void quant_unit(bool go, bool is_key, int part, RowF 
         const int t = t0 + i * RPL;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         old[i] = make_uint2(0u, 0u);
-        if (go && t >= n_old && t < m) x[i] = ld_nc_v4(new_row(t) + chunk * 8);
+        if (go && t >= n_old && t < m) x[i] = ld_nc_v4(src + t * stride + chunk * 8);
     }
     if (go && n_old > 0) {
         s_old = *scale;
@@ -348,7 +350,7 @@ __device__ __forceinline__ void quant_unit(bool go, bool is_key, int part, RowF 
 // Prefill write: grid (ceil(max_pages / QZ_PAGES_PER_BLOCK), B), pages from the one holding first_pos[b]
 // on.  Request b's new rows start in the packed input after those of requests 0..b-1.
 template <int D, int WPU, int FMT>
-__global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_prefill(const CentroidArgs a, const QuantArgs qa) {
+__global__ void __launch_bounds__(QZ_WARPS * 32, 4) k_quant_prefill(const CentroidArgs a, const QuantArgs qa) {
     constexpr int UNITS = QZ_WARPS / WPU;  // units in flight per block
     __shared__ uint32_t s_max[QZ_WARPS];
     __shared__ float s_sum[WPU > 1 ? QZ_WARPS : 1][D];
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_prefill(const CentroidA
             float *scale;
             __nv_bfloat16 *centroid;
             const bool ok = page(codes, scale, centroid) && go;
-            quant_unit<D, WPU, FMT>(ok, is_key, warp % WPU, new_row, codes, scale, centroid, max(0, fp - j * a.P), m,
+            quant_unit<D, WPU, FMT>(ok, is_key, warp % WPU, src, (int64_t)a.Hkv * D, codes, scale, centroid, max(0, fp - j * a.P), m,
                                     a.err, lane, s_max, s_sum);
         } else {
             quant_new_unit<D, WPU, FMT>(go, is_key, warp % WPU, new_row, page, m, a.err, lane, s_max, s_sum);
