@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
     if (item >= rows * a.G * NSLICE) return;
     const int slice = static_cast<int>(item % NSLICE);
     const int64_t rg = item / NSLICE;
-    const int64_t r = rg / a.G;
-    const int g = static_cast<int>(rg % a.G);
+    const int64_t r = div64(rg, a.G);
+    const int g = static_cast<int>(rg - r * a.G);
     const int64_t c_lo = piece_of(r * a.units_per_row, a.units, a.static_units, a.static_chunks, a.chunks);
     const int64_t c_hi = piece_of((r + 1) * a.units_per_row - 1, a.units, a.static_units, a.static_chunks, a.chunks);
     const int np = static_cast<int>(c_hi - c_lo + 1);
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
             for (int u = 0; u < GROUP; ++u) add(v[u], __shfl_sync(FULL, w_lane, u));
         }
     }
-    const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
+    const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
     const size_t head = (size_t)b * a.Hq + (size_t)h * a.G + g;
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
     __nv_bfloat16 *dst = a.out + head * DV + slice * SLICE + lane * PER;

@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     auto start_row = [&](int64_t r) {
         v_ref = DQ_VMIN;
         v_inv = 1.f / DQ_VMIN;
-        const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
+        const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
         const __nv_bfloat16 *qb = a.q + ((size_t)b * a.Hq + (size_t)h * a.G) * D;
         load_query<D, NT>(qb, a.G, a.scale_log2, qf, hs, lane);
 #pragma unroll
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     // attended tiles get theirs overwritten later by this same warp
     auto empty_piece = [&](int64_t c) {
         const int64_t u0 = p_start(c), u1 = p_start(c + 1);
-        for (int64_t r = u0 / a.units_per_row; r <= (u1 - 1) / a.units_per_row; ++r)
+        for (int64_t r = div64(u0, a.units_per_row); r <= div64(u1 - 1, a.units_per_row); ++r)
             if (lane < a.G) {
                 float *ml = a.ml_part + ((r + c) * a.G + lane) * 2;
                 ml[0] = -INFINITY;
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
         ks = __ldg(k_scale + rs.z);
         vs = __ldg(v_scale + rs.z);
     }
-    const int b = static_cast<int>(r / a.Hkv), h = static_cast<int>(r % a.Hkv);
+    const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
     uint32_t qf[NT][MT][2];
     float hs[NT][2], acc[NT][MT][4], m_run[NT][2], l_run[NT][2];
     float v_ref = DQ_VMIN, v_inv = 1.f / DQ_VMIN;

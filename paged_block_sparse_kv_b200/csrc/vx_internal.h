@@ -267,13 +267,18 @@ cudaError_t ensure_smem_limit(F kern, int bytes, std::atomic<unsigned long long>
 
 // warps per block of the 8-bit decode for groups of G query heads
 __host__ __device__ constexpr int quant_warps(int G) { return G <= 8 ? DQ_WARPS : DQ_WARPS_WIDE; }
+// a / b for 0 <= a, 0 < b: in 32 bits where both fit (a quarter of the instructions)
+__host__ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
 // chunk c of W covers units [c*T/W, (c+1)*T/W)
 __host__ __device__ __forceinline__ int64_t chunk_start(int64_t c, int64_t T, int64_t W) {
-    return (c * T) / W;
+    return div64(c * T, W);
 }
 // the chunk holding unit u
 __host__ __device__ __forceinline__ int64_t chunk_of(int64_t u, int64_t T, int64_t W) {
-    return ((u + 1) * W - 1) / T;
+    return div64((u + 1) * W - 1, T);
 }
 
 // Pieces of the decode split: pieces 0 .. Ws-1 cut units [0, Us) into Ws equal chunks, pieces
