@@ -26,12 +26,18 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "vx_attend.cuh"
 
 namespace vx {
 
 namespace {
 
+// Partials per row above which the merge takes a block per row and head (k_merge_many).  Against
+// k_merge, us per call: 85 partials per row 20.0 and 20.7, 296 15.6 and 18.5, 1,024 23.4 and 33.7; but
+// 18 per row 23.0 and 21.9.
+constexpr int DQ_MANY = 32;
 constexpr float DQ_PSHIFT = 15.f;  // weights are at most 2^15, fp16's largest number is 65504
 constexpr float DQ_VMIN = 0x1p-126f;  // v_ref of a row without a tile: the smallest normal number
 // 16-token tiles in flight per warp (4 KB each at head_dim 128): about 192 KB per SM
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     }
     __syncwarp();
 
-    const int64_t wid = (int64_t)blockIdx.x * WARPS + warp;
+    const int64_t wid = (int64_t)warp * gridDim.x + blockIdx.x;  // few chunks still reach every SM
     if (wid >= a.static_chunks) return;
 
     uint32_t qf[NT][MT][2];
@@ -502,6 +508,91 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     }
 }
 
+// Partials (unnormalised output, maximum in log2 units, sum) of one row and query head, joined in
+// order by a warp; D / 32 dims per lane.
+template <int D>
+struct Joined {
+    static constexpr int PER = D / 32;
+    using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+    float o[PER], m = -INFINITY, l = 0.f;
+
+    __device__ __forceinline__ Joined() {
+#pragma unroll
+        for (int d = 0; d < PER; ++d) o[d] = 0.f;
+    }
+    // n partials, `stride` heads apart: the maximum of all first, then the weighted sums; an empty
+    // one (maximum -inf) left no output
+    __device__ __forceinline__ void add_all(const float *op, const float *ml, int64_t stride, int n, int lane) {
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i * stride * 2]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
+        if (m == -INFINITY) return;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            Vec v[8];
+            float w[8], li[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = min(i0 + u, n - 1);
+                v[u] = *reinterpret_cast<const Vec *>(op + i * stride * D + lane * PER);
+                w[u] = ml[i * stride * 2];
+                li[u] = ml[i * stride * 2 + 1];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (i0 + u >= n || w[u] == -INFINITY) continue;
+                const float f = exp2f(w[u] - m);
+                const float *x = reinterpret_cast<const float *>(&v[u]);
+                l += f * li[u];
+#pragma unroll
+                for (int d = 0; d < PER; ++d) o[d] += f * x[d];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float *op, float *ml, int lane) const {
+        *reinterpret_cast<Vec *>(op + lane * PER) = *reinterpret_cast<const Vec *>(o);
+        if (lane == 0) {
+            ml[0] = m;
+            ml[1] = l;
+        }
+    }
+    __device__ __forceinline__ void finish(const DecodeArgs &a, int64_t r, int g, int lane) const {
+        const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
+        const size_t head = (size_t)b * a.Hq + (size_t)h * a.G + g;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + head * D + lane * PER);
+#pragma unroll
+        for (int d = 0; d < PER; d += 2) dst[d / 2] = pack_bf16x2(o[d] * inv, o[d + 1] * inv);
+        if (a.lse && lane == 0) a.lse[head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+};
+
+// Merge of rows with many partials: a block per (row, query head), whose 8 warps take the partials in
+// turn and meet in shared memory, in warp order.
+template <int D>
+__global__ void __launch_bounds__(256) k_merge_many(const DecodeArgs a) {
+    __shared__ __align__(16) float s_o[8][D];
+    __shared__ float s_ml[8][2];
+    pdl_wait();
+    pdl_trigger();  // the next grid may land; it waits for this grid's end
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = blockIdx.x;
+    const int g = blockIdx.y;
+    auto piece = [&](int64_t u) { return piece_of(u, a.units, a.static_units, a.static_chunks, a.chunks); };
+    const int64_t lo = piece(r * a.units_per_row);
+    const int n = static_cast<int>(piece((r + 1) * a.units_per_row - 1) - lo + 1);
+    Joined<D> j;
+    if (warp < n)
+        j.add_all(a.o_part + ((r + lo + warp) * a.G + g) * D, a.ml_part + ((r + lo + warp) * a.G + g) * 2, a.G * 8,
+                  (n - warp + 7) / 8, lane);
+    j.store(s_o[warp], s_ml[warp], lane);
+    __syncthreads();
+    if (warp > 0) return;
+    Joined<D> all;
+    all.add_all(s_o[0], s_ml[0], 1, min(n, 8), lane);
+    all.finish(a, r, g, lane);
+}
+
 // One block per (request, KV head) row of at most DQ_ROW_TILES tiles: warp w attends tiles 2 w and
 // 2 w + 1 (and 2 (w + WARPS), ...), and the warps' partials meet in shared memory, in warp order:
 // no partial goes through memory and no merge kernel follows.
@@ -656,8 +747,12 @@ cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorM
     static std::atomic<unsigned long long> done[2];
     cudaError_t e = ensure_smem_limit(kern, (int)smem, done[late ? 1 : 0]);
     if (e != cudaSuccess) return e;
-    return launch_k(kern, dim3(grid), dim3(WARPS * 32), smem, s, pdl, tmK, tmV, a, (const float *)qa.k_scale,
-                    (const float *)qa.v_scale);
+    e = launch_k(kern, dim3(grid), dim3(WARPS * 32), smem, s, pdl, tmK, tmV, a, (const float *)qa.k_scale,
+                 (const float *)qa.v_scale);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)a.B * a.Hkv, per_row = a.chunks / rows;
+    if (per_row > DQ_MANY) return launch_k(k_merge_many<D>, dim3((unsigned)rows, a.G), dim3(256), 0, s, true, a);
+    return launch_merge(a, s, true);
 }
 
 template <int D, int NT>

@@ -138,8 +138,10 @@ struct Plan {
 };
 
 
-// warps: worker warps of a GQA decode block
-vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p, int warps = vx::DEC_WARPS) {
+// warps: worker warps of a GQA decode block.  quant: the 8-bit decode's rule for the planned chunks,
+// which are dealt out to all SMs.
+vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p, int warps = vx::DEC_WARPS,
+               bool quant = false) {
     p->mla = g->mla_shared_kv != 0;
     p->G = g->num_q_heads / g->num_kv_heads;
     p->rows = (int64_t)g->batch * g->num_kv_heads;
@@ -148,10 +150,18 @@ vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p, int
     p->units = p->rows * p->units_per_row;
     const bool planned = num_splits <= 0;
     int64_t w = num_splits;
+    int sms = 0;
     if (planned) {
-        int sms = 0;
         if (sm_count_current(&sms) != 0) return fail(VX_ERR_CUDA, "cannot query the current device's SM count");
         w = p->mla ? (int64_t)sms : (int64_t)sms * warps;  // MLA: one CTA per SM
+        if (quant) {
+            // an even number of tiles per chunk (they are attended in pairs), at least 4, or 2 when 4
+            // would leave most SMs without a chunk.  Chunks and us against one chunk per warp: 16,384
+            // tiles in chunks of 8 21.2 and 22.3, 10,192 of 6 18.5 and 20.3, 4,096 of 4 10.8 and 12.4
+            int64_t per = std::max<int64_t>((p->units + w - 1) / w, p->units >= 4 * sms ? 4 : 2);
+            per += per & 1;
+            w = (p->units + per - 1) / per;
+        }
     }
     if (w > p->units) w = p->units;
     if (w < 1) w = 1;
@@ -184,6 +194,7 @@ vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p, int
     p->static_chunks = static_cast<int32_t>(ws_);
     p->chunks = static_cast<int32_t>(ws_ + wd);
     p->grid = p->mla ? p->chunks : (p->static_chunks + warps - 1) / warps;
+    if (quant && planned) p->grid = std::max(p->grid, std::min(p->static_chunks, sms));
     return VX_OK;
 }
 
@@ -271,7 +282,7 @@ size_t decode_ws_bytes(const WsLayout &l) { return l.scores; }
 // SMs the second wave costs more: 256 rows of 32 tiles 15.6 and 16.2, 512 rows of 8 tiles 11.9 and
 // 18.7.
 vx_status plan_quant(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
-    VX_TRY(plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads)));
+    VX_TRY(plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads), true));
     int sms = 0;
     p->by_row = num_splits <= 0 && p->units_per_row <= vx::DQ_ROW_TILES && sm_count_current(&sms) == 0 && p->rows <= sms;
     return VX_OK;
@@ -426,7 +437,7 @@ vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q,
         // (always with a programmatic launch: the kernel reads nothing before its dependency wait)
         if (p.by_row) a.chunks = 0;
         e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.by_row ? (int)p.rows : p.grid, s, true);
-        if (p.by_row) return e == cudaSuccess ? VX_OK : cuda_fail(e, "sparse decode launch");
+        return e == cudaSuccess ? VX_OK : cuda_fail(e, "sparse decode launch");
     } else if (p.mla) {
         CUtensorMap tmK, tmQ;
         VX_TRY(make_cache_map_blocks(&tmK, k_cache, g->head_dim_qk, g->page_size, page_heads,

@@ -194,8 +194,8 @@ cudaError_t launch_decode_gqa(const DecodeArgs &a, const CUtensorMap &tmK, const
 // grid = split count (one CTA per split); tmQ views q as (64 columns, rows = batch * Hq, 9 blocks)
 cudaError_t launch_decode_mla(const DecodeArgs &a, const CUtensorMap &tmK, const CUtensorMap &tmQ, int grid,
                               cudaStream_t s, bool pdl);
-// grid: blocks of quant_warps(G) warps; a.chunks == 0: one block per row, which writes out and lse
-// itself (no merge).  tmK and tmV view the codes as (head_dim, page_size, page-heads)
+// grid: blocks of quant_warps(G) warps; a.chunks == 0: one block per row.  Writes out and lse (the
+// merge kernel included).  tmK and tmV view the codes as (head_dim, page_size, page-heads)
 cudaError_t launch_decode_quant(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK,
                                 const CUtensorMap &tmV, int grid, cudaStream_t s, bool pdl);
 // a.k_cache, a.v_cache unused; mode CEN_APPEND or CEN_PREFILL
