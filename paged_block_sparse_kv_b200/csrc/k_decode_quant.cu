@@ -38,6 +38,7 @@ namespace {
 // k_merge, us per call: 85 partials per row 20.0 and 20.7, 296 15.6 and 18.5, 1,024 23.4 and 33.7; but
 // 18 per row 23.0 and 21.9.
 constexpr int DQ_MANY = 32;
+constexpr int DQ_FEW = 4;            // at most this many: k_merge_few
 constexpr float DQ_PSHIFT = 15.f;  // weights are at most 2^15, fp16's largest number is 65504
 constexpr float DQ_VMIN = 0x1p-126f;  // v_ref of a row without a tile: the smallest normal number
 // 16-token tiles in flight per warp (4 KB each at head_dim 128): about 192 KB per SM
@@ -593,6 +594,45 @@ __global__ void __launch_bounds__(256) k_merge_many(const DecodeArgs a) {
     all.finish(a, r, g, lane);
 }
 
+// Merge of rows with at most DQ_FEW partials: a warp per (row, query head), every load issued at once.
+template <int D>
+__global__ void __launch_bounds__(256, 6) k_merge_few(const DecodeArgs a) {
+    pdl_wait();
+    pdl_trigger();  // the next grid may land; it waits for this grid's end
+    const int lane = threadIdx.x & 31;
+    const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const uint32_t r = item / (uint32_t)a.G, g = item - r * (uint32_t)a.G;
+    if (r >= (uint32_t)a.B * (uint32_t)a.Hkv) return;
+    auto piece = [&](int64_t u) { return piece_of(u, a.units, a.static_units, a.static_chunks, a.chunks); };
+    const int64_t lo = piece((int64_t)r * a.units_per_row);
+    const int n = static_cast<int>(piece(((int64_t)r + 1) * a.units_per_row - 1) - lo + 1);
+    using J = Joined<D>;
+    const float *op = a.o_part + ((r + lo) * a.G + g) * D + lane * J::PER, *ml = a.ml_part + ((r + lo) * a.G + g) * 2;
+    typename J::Vec v[DQ_FEW];
+    float2 s[DQ_FEW];
+#pragma unroll
+    for (int i = 0; i < DQ_FEW; ++i) {
+        s[i] = make_float2(-INFINITY, 0.f);
+        if (i < n) {
+            s[i] = *reinterpret_cast<const float2 *>(ml + (int64_t)i * a.G * 2);
+            v[i] = *reinterpret_cast<const typename J::Vec *>(op + (int64_t)i * a.G * D);
+        }
+    }
+    J j;
+#pragma unroll
+    for (int i = 0; i < DQ_FEW; ++i) j.m = fmaxf(j.m, s[i].x);
+#pragma unroll
+    for (int i = 0; i < DQ_FEW; ++i) {
+        if (s[i].x == -INFINITY) continue;  // an empty partial left no output
+        const float f = exp2f(s[i].x - j.m);
+        const float *x = reinterpret_cast<const float *>(&v[i]);
+        j.l += f * s[i].y;
+#pragma unroll
+        for (int d = 0; d < J::PER; ++d) j.o[d] += f * x[d];
+    }
+    j.finish(a, r, (int)g, lane);
+}
+
 // One block per (request, KV head) row of at most DQ_ROW_TILES tiles: warp w attends tiles 2 w and
 // 2 w + 1 (and 2 (w + WARPS), ...), and the warps' partials meet in shared memory, in warp order:
 // no partial goes through memory and no merge kernel follows.
@@ -752,6 +792,11 @@ cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorM
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.Hkv, per_row = a.chunks / rows;
     if (per_row > DQ_MANY) return launch_k(k_merge_many<D>, dim3((unsigned)rows, a.G), dim3(256), 0, s, true, a);
+    // pieces that a row can span: of the even or static part, and of the late one
+    int64_t most = div64(a.units_per_row * a.static_chunks + a.static_units - 1, a.static_units) + 1;
+    if (late) most += div64(a.units_per_row * (a.chunks - a.static_chunks) + a.units - a.static_units - 1, a.units - a.static_units) + 1;
+    if (most <= DQ_FEW)
+        return launch_k(k_merge_few<D>, dim3((unsigned)((rows * a.G + 7) / 8)), dim3(256), 0, s, true, a);
     return launch_merge(a, s, true);
 }
 
