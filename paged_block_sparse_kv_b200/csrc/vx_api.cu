@@ -434,9 +434,11 @@ vx_status do_decode(const vx_geometry *g, const vx_page_table *t, const void *q,
         CUtensorMap tmK, tmV;
         VX_TRY(make_code_map(&tmK, quant->k_cache, g->head_dim_qk, g->page_size, page_heads));
         VX_TRY(make_code_map(&tmV, quant->v_cache, g->head_dim_v, g->page_size, page_heads));
-        // (always with a programmatic launch: the kernel reads nothing before its dependency wait)
+        // launched early also in plain stream order: the kernel reads nothing before its dependency
+        // wait.  (Not behind the memset of the late pieces' counter.)
+        const bool early = pdl || p.chunks == p.static_chunks;
         if (p.by_row) a.chunks = 0;
-        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.by_row ? (int)p.rows : p.grid, s, true);
+        e = vx::launch_decode_quant(a, quant_args(quant), tmK, tmV, p.by_row ? (int)p.rows : p.grid, s, early);
         return e == cudaSuccess ? VX_OK : cuda_fail(e, "sparse decode launch");
     } else if (p.mla) {
         CUtensorMap tmK, tmQ;

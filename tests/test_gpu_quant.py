@@ -180,6 +180,17 @@ def test_decode_late_pieces():
     check_attention(out[:3], lse[:3], want)
     again, lse2 = decode(c, cache, q.to(DEV), d_sel)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+    # the same from a graph, with the counter reset inside
+    ws = torch.empty(vx.vx_workspace_size(c.geo, c.max_pages, k), dtype=torch.uint8, device=DEV)
+    d_q, graph = q.to(DEV), torch.cuda.CUDAGraph()
+    out3, lse3 = torch.zeros_like(out), torch.zeros_like(lse)
+    with torch.cuda.graph(graph):
+        vx.vx_sparse_decode_quant(c.geo, c.table, d_q, cache, d_sel, k, out3, ws, lse=lse3)
+    for _ in range(3):
+        ws.random_(0, 256)
+        out3.zero_()
+        graph.replay()
+        assert torch.equal(out, out3) and torch.equal(lse, lse3)
 
 
 def test_decode_bad_entries_are_reported_and_skipped():
