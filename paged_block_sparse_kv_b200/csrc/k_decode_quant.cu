@@ -633,14 +633,13 @@ __global__ void __launch_bounds__(256, 6) k_merge_few(const DecodeArgs a) {
     j.finish(a, r, (int)g, lane);
 }
 
-// One block per (request, KV head) row of at most DQ_ROW_TILES tiles: warp w attends tiles 2 w and
-// 2 w + 1 (and 2 (w + WARPS), ...), and the warps' partials meet in shared memory, in warp order:
-// no partial goes through memory and no merge kernel follows.
-template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
+// One block of WARPS warps per (request, KV head) row of at most WARPS * SLOTS tiles: warp w attends
+// tiles 2 w and 2 w + 1 (and 2 (w + WARPS), ...), and the warps' partials meet in shared memory, in
+// warp order: no partial goes through memory and no merge kernel follows.
+template <int D, int NT, int FMT, int WARPS, int SLOTS>
+__global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
     k_decode_quant_row(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const DecodeArgs a, const float *__restrict__ k_scale, const float *__restrict__ v_scale) {
-    constexpr int WARPS = quant_warps(NT * 8), SLOTS = DQ_ROW_TILES / WARPS;  // tiles of a warp, loaded at once
     constexpr int TILE_BYTES = DEC_TILE * D, MT = D / 16;
     static_assert(SLOTS % 2 == 0, "tiles go in pairs");
     __shared__ uint64_t s_bar[WARPS];
@@ -768,19 +767,28 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     }
 }
 
+template <int D, int NT, int FMT, int WARPS, int SLOTS>
+cudaError_t launch_row(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                       cudaStream_t s, bool pdl) {
+    constexpr size_t tiles = (size_t)WARPS * SLOTS * 2 * DEC_TILE * D, parts = (size_t)WARPS * NT * 8 * D * 4;
+    constexpr size_t smem = 1024 + (tiles > parts ? tiles : parts);
+    auto kern = k_decode_quant_row<D, NT, FMT, WARPS, SLOTS>;
+    static std::atomic<unsigned long long> done;
+    const cudaError_t e = ensure_smem_limit(kern, (int)smem, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kern, dim3((unsigned)((int64_t)a.B * a.Hkv)), dim3(WARPS * 32), smem, s, pdl, tmK, tmV, a,
+                    (const float *)qa.k_scale, (const float *)qa.v_scale);
+}
+
 template <int D, int NT, int FMT>
 cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorMap &tmK, const CUtensorMap &tmV,
                        int grid, cudaStream_t s, bool pdl) {
     constexpr int WARPS = quant_warps(NT * 8);
     const size_t smem = 1024 + (size_t)WARPS * dq_stages(WARPS) * (2 * DEC_TILE * D + 8 + sizeof(QuantMeta) + sizeof(int32_t));
-    if (a.chunks == 0) {  // a block per row
-        constexpr size_t tiles = (size_t)DQ_ROW_TILES * 2 * DEC_TILE * D, parts = (size_t)WARPS * NT * 8 * D * 4;
-        const size_t row_smem = 1024 + (tiles > parts ? tiles : parts);
-        static std::atomic<unsigned long long> row_done;
-        cudaError_t e = ensure_smem_limit(k_decode_quant_row<D, NT, FMT>, (int)row_smem, row_done);
-        if (e != cudaSuccess) return e;
-        return launch_k(k_decode_quant_row<D, NT, FMT>, dim3(grid), dim3(WARPS * 32), row_smem, s, pdl, tmK, tmV, a,
-                        (const float *)qa.k_scale, (const float *)qa.v_scale);
+    if (a.chunks == 0) {  // a block per row, of the fewest warps that hold its tiles
+        if (a.units_per_row <= 8) return launch_row<D, NT, FMT, 4, 2>(a, qa, tmK, tmV, s, pdl);
+        if (a.units_per_row <= 16) return launch_row<D, NT, FMT, WARPS / 2, 32 / WARPS>(a, qa, tmK, tmV, s, pdl);
+        return launch_row<D, NT, FMT, WARPS, DQ_ROW_TILES / WARPS>(a, qa, tmK, tmV, s, pdl);
     }
     const bool late = a.chunks > a.static_chunks;
     auto kern = late ? k_decode_quant<D, NT, FMT, true> : k_decode_quant<D, NT, FMT, false>;

@@ -276,15 +276,16 @@ WsLayout ws_layout(const vx_geometry *g, int32_t max_pages, int32_t k, const Pla
 size_t decode_ws_bytes(const WsLayout &l) { return l.scores; }
 
 // the 8-bit decode's plan: the same split rule for its own count of warps
-// Planned, and with no more rows than SMs and short rows: a block per row, whose warps join their
-// partials in shared memory, instead of a split over the GPU and the merge kernel.  Measured, split
-// and row (us): 8 rows of 8 tiles 8.6 and 4.7, 128 rows of 32 tiles 11.4 and 8.3; with more rows than
-// SMs the second wave costs more: 256 rows of 32 tiles 15.6 and 16.2, 512 rows of 8 tiles 11.9 and
-// 18.7.
+// Planned, short rows, and no more of them than fit the GPU at once: a block per row, whose warps join
+// their partials in shared memory, instead of a split over the GPU and a merge kernel.  Measured,
+// split and row (us): 32 rows of 8 tiles 7.9 and 4.4, 128 of 32 10.8 and 8.1, 256 of 16 10.3 and 7.3,
+// 512 of 8 10.3 and 7.7; a second wave costs more: 256 of 32 14.5 and 16.3, 512 of 16 15.5 and 15.8,
+// 2,048 of 8 24.6 and 28.4.
 vx_status plan_quant(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
     VX_TRY(plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads), true));
     int sms = 0;
-    p->by_row = num_splits <= 0 && p->units_per_row <= vx::DQ_ROW_TILES && sm_count_current(&sms) == 0 && p->rows <= sms;
+    p->by_row = num_splits <= 0 && p->units_per_row <= vx::DQ_ROW_TILES && sm_count_current(&sms) == 0 &&
+                p->rows <= (int64_t)sms * vx::row_blocks_per_sm(p->G, p->units_per_row);
     return VX_OK;
 }
 

@@ -267,6 +267,11 @@ cudaError_t ensure_smem_limit(F kern, int bytes, std::atomic<unsigned long long>
 
 // warps per block of the 8-bit decode for groups of G query heads
 __host__ __device__ constexpr int quant_warps(int G) { return G <= 8 ? DQ_WARPS : DQ_WARPS_WIDE; }
+// blocks of the 8-bit decode by rows that an SM holds: rows of up to 8, 16 and DQ_ROW_TILES tiles take
+// 4, 8 and 16 warps (4, 4 and 8 of twice the registers with more than 8 query heads); 0: not built
+__host__ __device__ constexpr int row_blocks_per_sm(int G, int64_t tiles) {
+    return tiles > DQ_ROW_TILES ? 0 : tiles > 16 ? 1 : tiles > 8 || G > 8 ? 2 : 4;
+}
 // a / b for 0 <= a, 0 < b: in 32 bits where both fit (a quarter of the instructions)
 __host__ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
     if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
