@@ -109,6 +109,30 @@ def test_copy_refuses_ambiguous_pairs():
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("n", [300, 513, 900])
+@pytest.mark.parametrize("same", [True, False])
+def test_copy_random_pairs(n, same):
+    """Pairs with repeated destinations, sources that are destinations and bad ids, fewer and more than a block checks
+    by itself."""
+    rng = np.random.default_rng(n)
+    pages = 800
+    dst = Pool("int8", pages, Hkv=1, D=64, P=16, seed=1)
+    src = dst if same else Pool("int8", pages, Hkv=1, D=64, P=16, seed=2)
+    s, d = rng.integers(-2, pages // 2, n), rng.integers(pages // 4, pages + 2, n)
+    err = err_word()
+    vx.vx_copy_pages(dst.geo, src.vx, dst.vx, dev(s), dev(d), workspace(dst.geo), err=err)
+    named, sources = set(), set(s.tolist()) if same else set()
+    before = [a.copy() for a in src.host]
+    for x, y in zip(s.tolist(), d.tolist()):
+        if 0 <= y < pages and y not in named:
+            if 0 <= x < pages and y not in sources:
+                for a, b in zip(dst.host, before):
+                    a[y] = b[x]
+            named.add(y)
+    dst.check()
+    assert int(err.item()) == vx.VX_DATA_BAD_COPY | vx.VX_DATA_BAD_PAGE_ID
+
+
 def test_copy_far_pages():
     """Pages whose bytes lie past 2^32 from the pool's start."""
     n = 70000  # x 8 x 32 x 128 x 2 bytes = 4.6 GB each for K and V
@@ -318,11 +342,12 @@ def test_compact(kind, in_place, share):
     _compact(pool, rows, lens, refs, max(1, max(len(r) for r in rows)), in_place)
 
 
-@pytest.mark.parametrize("pages", [1, 2, 127, 128, 1025, 33000, 280001])
-def test_compact_pool_sizes(pages):
+@pytest.mark.parametrize("pages", [1, 2, 127, 128, 1025, 4095, 4096, 4097, 8193, 33000, 280001])
+@pytest.mark.parametrize("share", [0.6, 0.0, 1.0])
+def test_compact_pool_sizes(pages, share):
     rng = np.random.default_rng(pages)
     pool = Pool("int8", pages, seed=8, Hkv=1, D=64, P=16)
-    refs = (rng.random(pages) < 0.6) * rng.integers(1, 4, pages)
+    refs = (rng.random(pages) < share) * rng.integers(1, 4, pages)
     live = np.flatnonzero(refs)
     rows = [list(live[::2]), list(live[1::2])]
     _compact(pool, rows, [16 * len(r) for r in rows], refs, max(1, pages), False)
