@@ -83,11 +83,14 @@ struct PoolRanks {
     const uint32_t *pre;  // [groups + 1], shared
     int32_t segs, g, groups;
 
-    __device__ __forceinline__ PoolRanks(const PageArgs &a, uint32_t *s_pre, uint32_t *s_warp)
+    __device__ __forceinline__ PoolRanks(const PageArgs &a, const uint32_t *s_pre)
         : bits(a.list_a), counts(a.list_b), pre(s_pre) {
         segs = (int)((a.num_pages + PG_SEG - 1) / PG_SEG);
-        g = ceil_div(segs, PG_GROUPS);
-        groups = ceil_div(segs, g);
+        g = segs <= PG_GROUPS ? 1 : ceil_div(segs, PG_GROUPS);
+        groups = g == 1 ? segs : ceil_div(segs, g);
+    }
+    // the prefix sums, by the whole block
+    __device__ __forceinline__ void sum(uint32_t *s_pre, uint32_t *s_warp) const {
         // thread t sums groups [t * per, (t + 1) * per)
         const int per = ceil_div(groups, PG_BLOCK), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int k0 = min(groups, (int)threadIdx.x * per), k1 = min(groups, k0 + per);
@@ -117,7 +120,7 @@ struct PoolRanks {
     __device__ __forceinline__ uint32_t total() const { return pre[groups]; }
     // flagged pages before segment `seg`
     __device__ __forceinline__ uint32_t before_segment(int seg) const {
-        const int k = seg / g;
+        const int k = g == 1 ? seg : seg / g;
         uint32_t r = pre[k];
 #pragma unroll 1
         for (int s = k * g; s < seg; ++s) r += (uint32_t)counts[s];
@@ -433,8 +436,17 @@ __global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a, con
     }
     const uint32_t need = (uint32_t)a.head[1];
     const unsigned row_bad = (unsigned)a.head[0];
-    const PoolRanks free_pages(a, s_pre, s_warp);
-    const unsigned bad = row_bad ? row_bad : need > free_pages.total() ? VX_DATA_NO_PAGES : 0u;
+    PoolRanks free_pages(a, s_pre);
+    uint32_t total;
+    if (is_copy || is_fresh) {
+        free_pages.sum(s_pre, s_warp);
+        total = free_pages.total();
+    } else {  // the total alone, without a barrier
+        uint32_t c = 0;
+        for (int s = lane; s < free_pages.segs; s += 32) c += (uint32_t)free_pages.counts[s];
+        total = __reduce_add_sync(FULL, c);
+    }
+    const unsigned bad = row_bad ? row_bad : need > total ? VX_DATA_NO_PAGES : 0u;
     if (bad) {
         for (uint32_t i = blockIdx.x * PG_BLOCK + tid; i < (uint32_t)a.new_rows; i += gridDim.x * PG_BLOCK) a.new_lens[i] = 0;
         if (blockIdx.x == 0 && tid == 0) set_err(a.err, bad);
@@ -509,7 +521,8 @@ __global__ void __launch_bounds__(PG_BLOCK) k_list_compact(const PageArgs a) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const PoolRanks live(a, s_pre, s_warp);
+    PoolRanks live(a, s_pre);
+    live.sum(s_pre, s_warp);
     const uint32_t n = live.total();
     // live pages below page n
     uint32_t low = n;
