@@ -29,6 +29,7 @@ constexpr int PG_MAX_ROWS = 4096;
 constexpr int PG_PIECE = 1024;   // 16-byte chunks of a page moved by one block at a time
 constexpr int PG_SPAN = 256;     // table entries handled by one warp, 8 per lane
 constexpr int PG_BLOCK = 256;    // threads of an applying block
+constexpr int PG_RANKS = PG_BLOCK / 32 / 4 * PG_SEG;  // pages that a block handing out fresh ones looks at
 // Copies up to which every block checks its own pair (k_copy_few) instead of a planner checking all:
 // us with and without the planner: 5 pages of 35 KB 4.3 and 2.4, 256 6.4 and 5.3, 512 10.8 and 9.9, 1,024
 // 18.3 and 18.6, 4,096 55.7 and 81.6.
@@ -402,7 +403,8 @@ __host__ __forceinline__ bool update_jobs(const PageArgs &a, UpdateJobs *j) {
 
 __global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a, const UpdateJobs jobs) {
     __shared__ uint32_t s_pre[PG_GROUPS + 1], s_warp[PG_BLOCK / 32];
-    __shared__ int32_t s_off[PG_MAX_ROWS];
+    __shared__ int32_t s_row[PG_RANKS];  // fresh pages: the new row of a rank
+    extern __shared__ int32_t s_to[];    // [new_rows]
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31;
     const RowPlan *plans = reinterpret_cast<const RowPlan *>(a.list_c);
@@ -479,9 +481,37 @@ __global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a, con
             else if (const int d = j < whole ? dw : dt) atomicAdd(a.ref_out + id, d);
         }
     } else {  // the lowest `need` free pages to the rows in order
+        // this block's segments have ranks [r0, r0 + PG_RANKS); which row each belongs to: every row
+        // marks its first rank, and a running maximum fills the rest
         const int first = (int)(job * (PG_BLOCK / 32) / 4);
-        if (free_pages.before_segment(min(first, free_pages.segs - 1)) >= need) return;
-        for (int i = tid; i < a.new_rows; i += PG_BLOCK) s_off[i] = plans[i].off;
+        const uint32_t r0 = free_pages.before_segment(min(first, free_pages.segs - 1));
+        if (r0 >= need) return;
+        for (int e = tid; e < PG_RANKS; e += PG_BLOCK) s_row[e] = 0;
+        __syncthreads();
+        for (int i = tid; i < a.new_rows; i += PG_BLOCK) {
+            const RowPlan p = plans[i];
+            s_to[i] = a.new_ptr[i] + p.held - p.off;  // place of rank 0 in new_indices
+            const int64_t d = (int64_t)p.off - r0;
+            if (d < PG_RANKS) atomicMax(&s_row[d > 0 ? d : 0], i);
+        }
+        __syncthreads();
+        constexpr int PER = PG_RANKS / PG_BLOCK;
+        int32_t top[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) top[e] = max(s_row[tid * PER + e], e > 0 ? top[e - 1] : 0);
+        int32_t x = top[PER - 1];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t y = __shfl_up_sync(FULL, x, off);
+            if (lane >= off) x = max(x, y);
+        }
+        if (lane == 31) s_warp[tid >> 5] = (uint32_t)x;
+        x = __shfl_up_sync(FULL, x, 1);
+        if (lane == 0) x = 0;
+        __syncthreads();
+        for (int w = 0; w < (tid >> 5); ++w) x = max(x, (int32_t)s_warp[w]);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) s_row[tid * PER + e] = max(top[e], x);
         __syncthreads();
         const int seg = (int)(unit / 4), w0 = (int)(unit % 4) * 8;
         if (seg >= free_pages.segs) return;
@@ -493,13 +523,7 @@ __global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a, con
             const uint32_t r = __shfl_sync(FULL, rank0, w) + __popc(f & ((1u << lane) - 1u));
             if (!((f >> lane) & 1u) || r >= need) continue;
             const int32_t page = seg * PG_SEG + w * 32 + lane;
-            int lo = 0, hi = a.new_rows - 1;  // the last row whose fresh pages start at or before rank r
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if ((uint32_t)s_off[mid] <= r) lo = mid;
-                else hi = mid - 1;
-            }
-            a.new_indices[a.new_ptr[lo] + plans[lo].held + (int32_t)(r - (uint32_t)s_off[lo])] = page;
+            a.new_indices[s_to[s_row[r - r0]] + (int32_t)r] = page;
             a.ref_out[page] = 1;
         }
     }
@@ -681,7 +705,8 @@ cudaError_t launch_update_table(const PageArgs &a, cudaStream_t s) {
     if (!update_jobs(a, &j)) return cudaErrorInvalidValue;
     const uint32_t blocks = j.fresh + j.rows + j.refs + j.copies;
     cudaError_t e = launch_k(k_plan_update, dim3((unsigned)(1 + plan_blocks(a))), dim3(PG_THREADS), 0, s, true, a);
-    if (e == cudaSuccess) e = launch_k(k_apply_update, dim3((unsigned)blocks), dim3(PG_BLOCK), 0, s, true, a, j);
+    const size_t smem = (size_t)a.new_rows * sizeof(int32_t);
+    if (e == cudaSuccess) e = launch_k(k_apply_update, dim3((unsigned)blocks), dim3(PG_BLOCK), smem, s, true, a, j);
     return e;
 }
 
