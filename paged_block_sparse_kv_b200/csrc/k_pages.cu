@@ -175,9 +175,12 @@ __device__ __forceinline__ void copy_piece(const PageArgs &a, int64_t src, int64
     constexpr int U = PG_PIECE / PG_BLOCK;
     uint4 v[U];
     uint8_t *to[U];
+    // equal pieces (to a warp's 32 chunks): a short last one would cost a block as much as a whole one
+    const int size = (ceil_div(page_chunks(a), page_pieces(a)) + 31) & ~31;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        int c = piece * PG_PIECE + u * PG_BLOCK + (int)threadIdx.x;
+        const int k = u * PG_BLOCK + (int)threadIdx.x;
+        int c = k < size ? piece * size + k : INT32_MAX;
         const uint8_t *from = nullptr;
         to[u] = nullptr;
         if (c < nk) {
