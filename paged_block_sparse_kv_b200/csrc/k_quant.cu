@@ -147,10 +147,17 @@ __device__ __forceinline__ void quant_new_unit(bool go, bool is_key, int part, R
     constexpr int CPR = D / 8, RPL = 32 / CPR, NR = 16 / RPL;
     const int chunk = lane % CPR, t0 = part * 16 + lane / CPR;
     uint4 x[NR];
+    if (go && m == 16 * WPU) {
+        const __nv_bfloat16 *p = new_row(t0) + chunk * 8;
+        const int64_t step = new_row(RPL) - new_row(0);
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (go && t0 + i * RPL < m) x[i] = ld_nc_v4(new_row(t0 + i * RPL) + chunk * 8);
+        for (int i = 0; i < NR; ++i) x[i] = ld_nc_v4(p + i * step);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (go && t0 + i * RPL < m) x[i] = ld_nc_v4(new_row(t0 + i * RPL) + chunk * 8);
+        }
     }
     uint8_t *codes;
     float *scale;
@@ -173,13 +180,27 @@ __device__ __forceinline__ void quant_new_unit(bool go, bool is_key, int part, R
         sum[e] = 0.f;
     }
     if (go) {
+        // e4m3: scaled two at a time in bf16, exactly (s is a power of two; what falls below bf16's range
+        // is far below half the smallest code)
+        const __nv_bfloat162 inv2 = __float2bfloat162_rn(inv);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
+            if constexpr (FMT == VX_QUANT_E4M3) {
+                auto times = [&](uint32_t &w) {
+                    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w), inv2);
+                    w = *reinterpret_cast<const uint32_t *>(&y);
+                };
+                times(x[i].x);
+                times(x[i].y);
+                times(x[i].z);
+                times(x[i].w);
+            }
             float f[8];
             bf16x8_to_f32(x[i], f);
             uint32_t b[2][4] = {};
-            const uint2 c = make_uint2(four_codes<FMT>(f[0], f[1], f[2], f[3], inv, b[0]),
-                                       four_codes<FMT>(f[4], f[5], f[6], f[7], inv, b[1]));
+            const float by = FMT == VX_QUANT_E4M3 ? 1.f : inv;
+            const uint2 c = make_uint2(four_codes<FMT>(f[0], f[1], f[2], f[3], by, b[0]),
+                                       four_codes<FMT>(f[4], f[5], f[6], f[7], by, b[1]));
             if (t0 + i * RPL < m) *reinterpret_cast<uint2 *>(codes + (t0 + i * RPL) * D + chunk * 8) = c;
             if (is_key) {  // rows past m are zeros
                 if constexpr (FMT == VX_QUANT_INT8) {
