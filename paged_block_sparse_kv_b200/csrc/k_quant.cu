@@ -18,6 +18,10 @@
 //  * Append: a warp per unit; the one new row, and for the centroid the page's key codes in
 //    16-byte chunks.  Value codes are read only when the scale grows.  Latency bound (length ->
 //    table -> codes).
+// Measured on one B200: prefill of 8 requests, 16-token pages, head_dim 128 (833 MB): e4m3 147 us, int8
+// 149 us, 5.7 TB/s (0.86-0.87 of the copy peak); 64-token pages 155 us; head_dim 64 0.60-0.66 of it (a
+// unit is half as long and its fixed part the same).  Four blocks per SM (64 registers): three took
+// 156 us where four take 147 and two 174.  Append of 256 requests, 8 KV heads 5.6 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
