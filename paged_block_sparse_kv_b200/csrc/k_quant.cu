@@ -18,10 +18,12 @@
 //  * Append: a warp per unit; the one new row, and for the centroid the page's key codes in
 //    16-byte chunks.  Value codes are read only when the scale grows.  Latency bound (length ->
 //    table -> codes).
-// Measured on one B200: prefill of 8 requests, 16-token pages, head_dim 128 (833 MB): e4m3 147 us, int8
-// 149 us, 5.7 TB/s (0.86-0.87 of the copy peak); 64-token pages 155 us; head_dim 64 0.60-0.66 of it (a
-// unit is half as long and its fixed part the same).  Four blocks per SM (64 registers): three took
-// 156 us where four take 147 and two 174.  Append of 256 requests, 8 KV heads 5.6 us.
+// Measured on one B200: prefill of 8 requests, 16-token pages, head_dim 128 (833 MB): e4m3 139 us, int8
+// 144 us, 5.8-6.0 TB/s (0.89-0.92 of the copy peak); 64-token pages 154 us; head_dim 64 0.58-0.66 of it
+// (a unit is half as long and its fixed part the same).  Four blocks per SM (64 registers): three
+// took 156 us where four took 147 and two 174.  A grid of requests by pages, whose blocks past a short
+// request's end do nothing, took 148 us for the 8 ragged requests (and 486 where this one takes 507 for
+// 256 of equal length).  Append of 256 requests, 8 KV heads 5.6 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -374,54 +376,84 @@ __device__ __noinline__ void quant_unit(bool go, bool is_key, int part, const __
     }
 }
 
-// Prefill write: grid (ceil(units of the longest request / per_block), B); units page by page from the
-// one holding first_pos[b] on, a page's keys head by head, then its values.  Request b's new rows
-// start in the packed input after those of requests 0..b-1.
+// Inclusive sum over the block; total: the block's sum.  s_part: QZ_WARPS words.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_part, uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(FULL, v, off);
+        if (lane >= off) v += y;
+    }
+    if (lane == 31) s_part[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < QZ_WARPS; ++w) {
+        if (w < warp) v += s_part[w];
+        total += s_part[w];
+    }
+    __syncthreads();
+    return v;
+}
+
+// Prefill write.  The units of all requests form one flat list: the touched pages request by request
+// (request b's from the one holding first_pos[b] on), of a page the keys head by head, then the
+// values.  Block i takes units [i * per_block, (i + 1) * per_block); a table of the requests' first
+// pages in shared memory tells a warp whose unit it has.  Request b's new rows start in the packed
+// input after those of requests 0..b-1.
 template <int D, int WPU, int FMT>
 __global__ void __launch_bounds__(QZ_WARPS * 32, 4) k_quant_prefill(const CentroidArgs a, const QuantArgs qa, const int per_block) {
     constexpr int UNITS = QZ_WARPS / WPU;  // units in flight per block
-    __shared__ uint32_t s_max[QZ_WARPS];
+    __shared__ uint32_t s_max[QZ_WARPS], s_part[QZ_WARPS];
     __shared__ float s_sum[WPU > 1 ? QZ_WARPS : 1][D];
-    __shared__ long long s_part[QZ_WARPS];
+    // [B] (pages before the request's, its first row less first_pos, first_pos, length): with them at
+    // hand a unit's rows are asked for at once
+    extern __shared__ int4 s_req[];
     pdl_wait();
-    const int b = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t L = a.seq_lens[b], fp = a.first_pos[b];
-    const int j_lo = fp / a.P, heads2 = a.Hkv * 2;
-    const int64_t it_lo = (int64_t)blockIdx.x * per_block, units = (int64_t)(ceil_div(L, a.P) - j_lo) * heads2;
-    const bool sound = L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L;
-    if (sound && blockIdx.x > 0 && it_lo >= units) return;  // (block 0 checks the input's rows)
-    long long before = 0;
-    for (int i = threadIdx.x; i < b; i += blockDim.x) before += prefill_count(a, i);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(FULL, before, off);
-    if (lane == 0) s_part[warp] = before;
-    __syncthreads();
-    int64_t row0 = 0;
-#pragma unroll
-    for (int w = 0; w < QZ_WARPS; ++w) row0 += s_part[w];
-    if (!sound || row0 + (L - fp) > qa.num_new) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
-        return;
+    uint32_t rows = 0, pages = 0;  // of the requests so far
+    for (int b0 = 0; b0 < a.B; b0 += QZ_WARPS * 32) {
+        const int b = b0 + threadIdx.x;
+        const int32_t L = b < a.B ? a.seq_lens[b] : 0, fp = b < a.B ? a.first_pos[b] : 0;
+        bool sound = b < a.B && L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L;
+        const uint32_t n_new = sound ? L - fp : 0;
+        uint32_t total;
+        const uint32_t end = rows + block_scan(n_new, s_part, total);
+        rows += total;
+        sound = sound && end <= (uint64_t)qa.num_new;
+        if (b < a.B && !sound && blockIdx.x == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
+        const uint32_t n_pages = sound && L > fp ? ceil_div(L, a.P) - fp / a.P : 0;
+        const uint32_t last = pages + block_scan(n_pages, s_part, total);
+        pages += total;
+        if (b < a.B) s_req[b] = make_int4((int32_t)(last - n_pages), (int32_t)(end - n_new) - fp, fp, L);
     }
-    if (fp == L || it_lo >= units) return;
-    const int64_t it_hi = min(units, it_lo + per_block);
-    const int32_t *table = a.page_indices + a.page_ptr[b];
+    __syncthreads();
+    const int log2_p = __ffs(a.P) - 1;
+    const uint32_t heads2 = a.Hkv * 2;
+    const uint64_t units = (uint64_t)pages * heads2, it_lo = (uint64_t)blockIdx.x * per_block,
+                   it_hi = min(units, it_lo + per_block);
     const auto *kn = static_cast<const __nv_bfloat16 *>(a.k_new);
     const auto *vn = static_cast<const __nv_bfloat16 *>(a.v_new);
     auto *cen = static_cast<__nv_bfloat16 *>(a.centroids);
-    const int old_units = j_lo * a.P < fp ? heads2 : 0;  // those of a page that holds older tokens come first
-    for (int64_t it0 = it_lo; it0 < it_hi; it0 += UNITS) {
-        const int64_t it = it0 + warp / WPU;
-        const bool go = it < it_hi;
-        const int page_of = go ? (int)div64(it, heads2) : 0;
-        const int j = j_lo + page_of, rem = go ? (int)(it - (int64_t)page_of * heads2) : 0;
-        const bool is_key = rem < a.Hkv;
+    for (uint64_t it0 = it_lo; it0 < it_hi; it0 += UNITS) {
+        const bool go = it0 + warp / WPU < it_hi;
+        const uint64_t it = go ? it0 + warp / WPU : it0;
+        const uint32_t page_at = (uint32_t)div64((int64_t)it, heads2), rem = (uint32_t)(it - (uint64_t)page_at * heads2);
+        int b = 0, hi = a.B - 1;  // the last request whose pages start at or before this one
+        while (b < hi) {
+            const int mid = (b + hi + 1) >> 1;
+            if ((uint32_t)s_req[mid].x <= page_at) b = mid;
+            else hi = mid - 1;
+        }
+        const int4 req = s_req[b];
+        const int32_t L = req.w, fp = req.z;
+        const int j = (fp >> log2_p) + (int)(page_at - (uint32_t)req.x);
+        const int32_t id = a.page_indices[a.page_ptr[b] + j];
+        const bool is_key = rem < (uint32_t)a.Hkv;
         const int h = is_key ? rem : rem - a.Hkv;
-        const int m = min(a.P, L - j * a.P);
-        const __nv_bfloat16 *src = (is_key ? kn : vn) + ((row0 + (int64_t)j * a.P - fp) * a.Hkv + h) * D;
+        const int m = min(a.P, L - j * a.P), n_old = max(0, fp - j * a.P);
+        const __nv_bfloat16 *src = (is_key ? kn : vn) + (((int64_t)req.y + (int64_t)j * a.P) * a.Hkv + h) * D;
         auto new_row = [&](int t) { return src + (int64_t)t * a.Hkv * D; };
-        const int32_t id = table[j];
         auto page = [&](uint8_t *&codes, float *&scale, __nv_bfloat16 *&centroid) {
             const bool ok = id >= 0 && id < a.num_pool_pages;
             if (!ok && go && lane == 0) set_err(a.err, VX_DATA_BAD_PAGE_ID);
@@ -431,12 +463,14 @@ __global__ void __launch_bounds__(QZ_WARPS * 32, 4) k_quant_prefill(const Centro
             centroid = cen + blk * D;
             return ok;
         };
-        if (it0 < old_units) {  // (units of new pages may be among the UNITS too)
+        // units of several warps meet at barriers: their block takes one path
+        const bool old = WPU == 1 ? n_old > 0 : __syncthreads_or(n_old > 0);
+        if (old) {
             uint8_t *codes;
             float *scale;
             __nv_bfloat16 *centroid;
             const bool ok = page(codes, scale, centroid) && go;
-            quant_unit<D, WPU, FMT>(ok, is_key, warp % WPU, src, (int64_t)a.Hkv * D, codes, scale, centroid, max(0, fp - j * a.P), m,
+            quant_unit<D, WPU, FMT>(ok, is_key, warp % WPU, src, (int64_t)a.Hkv * D, codes, scale, centroid, n_old, m,
                                     a.err, lane, s_max, s_sum);
         } else {
             quant_new_unit<D, WPU, FMT>(go, is_key, warp % WPU, new_row, page, m, a.err, lane, s_max, s_sum);
@@ -600,15 +634,19 @@ cudaError_t launch_qdpf(const CentroidArgs &a, const QuantArgs &qa, int mode, cu
     } else {
         // a block takes one set of units after the other when there are many; a small write spreads
         // over the GPU (one request of 3,000 tokens on 4 heads, 64-token pages: 73 us with 8 pages
-        // per block)
+        // per block).  A request touches at most its new rows / P + 2 pages.
         constexpr int UNITS = QZ_WARPS / (P / 16);
-        const int64_t longest = (int64_t)a.max_pages * a.Hkv * 2, sets = (longest + UNITS - 1) / UNITS;
+        const int64_t pages = std::min(qa.num_new / P + 2 * (int64_t)a.B, (int64_t)a.B * a.max_pages);
+        const int64_t sets = (pages * a.Hkv * 2 + UNITS - 1) / UNITS;
         const int64_t resident = (int64_t)std::max(1, current_sm_count()) * 4;
-        const int64_t steps = std::min<int64_t>(QZ_MAX_STEPS, std::max<int64_t>(1, sets * a.B / (4 * resident)));
+        const int64_t steps = std::min<int64_t>(QZ_MAX_STEPS, std::max<int64_t>(1, sets / (4 * resident)));
         const int64_t blocks = (sets + steps - 1) / steps;
         if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-        return launch_k(k_quant_prefill<D, P / 16, FMT>, dim3((unsigned)blocks, a.B), dim3(QZ_WARPS * 32), 0, s, true, a,
-                        qa, (int)(steps * UNITS));
+        static std::atomic<unsigned long long> done;
+        const cudaError_t e = ensure_smem_limit(k_quant_prefill<D, P / 16, FMT>, 4096 * (int)sizeof(int4), done);
+        if (e != cudaSuccess) return e;
+        return launch_k(k_quant_prefill<D, P / 16, FMT>, dim3((unsigned)blocks), dim3(QZ_WARPS * 32),
+                        (size_t)a.B * sizeof(int4), s, true, a, qa, (int)(steps * UNITS));
     }
 }
 

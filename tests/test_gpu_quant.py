@@ -386,6 +386,31 @@ def test_write_bad_rows_are_reported_and_skipped():
     check_cache(c, cache, cen, want)
 
 
+@pytest.mark.parametrize("fmt,P", [("int8", 16), ("e4m3", 64), ("int8", 32)])
+def test_prefill_of_many_requests(fmt, P):
+    """More requests than a block has threads: chunks of every size, empty ones, some starting inside a page, and two
+    requests that are refused."""
+    B, rng = 600, np.random.default_rng(P)
+    L = rng.integers(1, 3 * P, B)
+    first = np.minimum(rng.integers(0, 3 * P, B), L)
+    first[::7] = L[::7]
+    c = Case(fmt, L, 1, 1, 64, P, seed=P).fill()
+    for s in (c.ks, c.vs):
+        s[:] = 2.0 ** np.rint(np.log2(s))
+    wrong = first.copy()
+    wrong[5], wrong[400] = L[5] + 1, -1
+    first[5], first[400] = L[5], L[400]  # their rows are not in the input
+    n = int((L - first).sum())
+    kn, vn = new_rows(c, n), new_rows(c, n)
+    cache, cen = c.cache(), torch.zeros(c.pool, 1, 64, dtype=torch.bfloat16, device=DEV)
+    want = np.zeros((c.pool, 1, 64))
+    vx.vx_quant_update(c.geo, c.table, cache, cen, kn.to(DEV), vn.to(DEV), first_pos=dev(wrong), err=c.err)
+    ref.quant_update(c.k, c.ks, want, kn.double().numpy(), c.ptr, c.idx, L, first, fmt)
+    ref.quant_update(c.v, c.vs, None, vn.double().numpy(), c.ptr, c.idx, L, first, fmt)
+    check_cache(c, cache, cen, want)
+    assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN
+
+
 def test_prefill_rows_past_the_input_are_refused():
     """Fewer new rows than the table says: the requests that would read past them write nothing."""
     c = Case("int8", [20, 30, 5], 2, 2, 64, 16, seed=1).blank()
