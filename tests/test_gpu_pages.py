@@ -511,3 +511,54 @@ def test_page_calls_captured_and_replayed():
         for x, y in zip((x for x in pool.t.values() if x is not None), host):
             assert np.array_equal(x.view(torch.uint8).cpu().numpy(), y)
         assert int(err.item()) == 0
+
+
+def test_pool_of_more_pages_than_prefix_sums():
+    """Over 2^20 pages: the ranks' prefix sums then stand for groups of segments."""
+    pages, P = 1_100_003, 16
+    geo = vx.Geometry(2, 1, 1, 64, 64, P, False, pages)
+    g = torch.Generator(DEV).manual_seed(3)
+    k = torch.randint(-128, 128, (pages, 1, P, 64), dtype=torch.int8, generator=g, device=DEV)
+    pool = vx.PagePool(k, k.clone())
+    refs = (torch.rand(pages, generator=g, device=DEV) < 0.7).to(torch.int32)
+    live = torch.nonzero(refs)[:, 0].to(torch.int32)
+    free = torch.nonzero(refs == 0)[:, 0]
+    n = int(live.numel())
+    half = n // 2
+    table = vx.PageTable(dev([0, half]), live[torch.randperm(n, generator=g, device=DEV)], dev([half * P, (n - half) * P - 5]),
+                         n - half)
+    ws, err = workspace(geo, 3), err_word()
+    # row 0 forked and grown by 200,000 pages, row 1 forked (its last page is copied)
+    more = 200_000
+    at1, at2 = half + more, n + more
+    rows = vx.PageTable(dev([0, at1, at2]), torch.full((2 * n + more,), -5, dtype=torch.int32, device=DEV),
+                        torch.zeros(3, dtype=torch.int32, device=DEV), n)
+    new_ref = torch.empty_like(refs)
+    before = k.clone()
+    vx.vx_update_table(geo, pool, table, refs, dev([0, 1, 1]), dev([more * P, 0, 0]), rows, new_ref, ws, err=err)
+    assert int(err.item()) == 0
+    idx = rows.page_indices
+    old0, old1 = table.page_indices[:half], table.page_indices[half:]
+    assert torch.equal(idx[:half], old0) and torch.equal(idx[half:half + more], free[:more].to(torch.int32))
+    assert torch.equal(idx[at1:at2], old1)
+    copied = int(free[more])
+    assert int(idx[at2 + n - half - 1]) == copied and torch.equal(idx[at2:at2 + n - half - 1], old1[:-1])
+    assert torch.equal(k[copied], before[int(old1[-1])])
+    want = refs.clone()
+    want[free[:more + 1]] = 1
+    want[old1[:-1].long()] += 1
+    assert torch.equal(new_ref, want)
+    # and packed
+    remap, count = torch.empty_like(refs), torch.zeros(1, dtype=torch.int32, device=DEV)
+    new_idx, packed = torch.full_like(table.page_indices, -5), torch.empty_like(refs)
+    before = k.clone()
+    vx.vx_compact_pages(geo, pool, table, new_ref, new_idx, packed, remap, count, ws, err=err)
+    m = int((new_ref > 0).sum())
+    ids = torch.arange(pages, device=DEV)
+    src, dst = ids[(new_ref > 0) & (ids >= m)], ids[(new_ref == 0) & (ids < m)]
+    want_map = torch.where(new_ref > 0, ids, torch.full_like(ids, -1))
+    want_map[src] = dst
+    assert int(count.item()) == m and torch.equal(remap.long(), want_map)
+    assert torch.equal(new_idx.long(), want_map[table.page_indices.long()])
+    assert torch.equal(k[dst], before[src]) and torch.equal(packed[dst], new_ref[src]) and int(packed[m:].sum()) == 0
+    assert int(err.item()) == 0

@@ -411,6 +411,47 @@ def test_prefill_of_many_requests(fmt, P):
     assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN
 
 
+def test_largest_batch():
+    """4,096 requests: append, prefill and attention."""
+    B, P, rng = 4096, 16, np.random.default_rng(1)
+    c = Case("int8", rng.integers(2, 40, B), 2, 1, 64, P, seed=9).blank()
+    cache, cen = c.cache(), torch.zeros(c.pool, 1, 64, dtype=torch.bfloat16, device=DEV)
+    want = np.zeros((c.pool, 1, 64))
+    for lo, hi in ((np.zeros(B, int), c.L - 1), (c.L - 1, c.L)):
+        t = vx.PageTable(c.table.page_ptr, c.table.page_indices, dev(hi), c.max_pages)
+        kn, vn = new_rows(c, int((hi - lo).sum())), new_rows(c, int((hi - lo).sum()))
+        vx.vx_quant_update(c.geo, t, cache, cen, kn.to(DEV), vn.to(DEV), first_pos=dev(lo) if lo[0] == 0 else None,
+                           err=c.err)
+        ref.quant_update(c.k, c.ks, want, kn.double().numpy(), c.ptr, c.idx, hi, lo, "int8")
+        ref.quant_update(c.v, c.vs, None, vn.double().numpy(), c.ptr, c.idx, hi, lo, "int8")
+    check_cache(c, cache, cen, want)
+    q, sel = c.queries(), c.select(3)
+    out, lse = decode(c, cache, q.to(DEV), dev(sel))
+    check_attention(out, lse, ref.attend(q.double().numpy(), *c.float_values(), c.ptr, c.idx, c.L, sel, 1 / 8))
+    assert int(c.err.item()) == 0
+
+
+def test_two_streams_at_once():
+    """The same cache read by two calls that run side by side, each with its own workspace and outputs."""
+    c = Case("e4m3", [3000, 500, 77], 16, 8, 128, 16, seed=41).fill()
+    sel, cache = c.select(60), c.cache()
+    d_sel = dev(sel)
+    qs = [c.queries() for _ in range(2)]
+    d_qs = [q.to(DEV) for q in qs]
+    ws = [torch.empty(vx.vx_workspace_size(c.geo, c.max_pages, 60), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i] = decode(c, cache, d_qs[i], d_sel, ws=ws[i])
+    torch.cuda.synchronize()
+    for q, (out, lse) in zip(qs, got):
+        check_attention(out, lse, ref.attend(q.double().numpy(), *c.float_values(), c.ptr, c.idx, c.L, sel,
+                                             1 / np.sqrt(128)))
+
+
 def test_prefill_rows_past_the_input_are_refused():
     """Fewer new rows than the table says: the requests that would read past them write nothing."""
     c = Case("int8", [20, 30, 5], 2, 2, 64, 16, seed=1).blank()
