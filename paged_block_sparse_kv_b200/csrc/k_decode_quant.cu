@@ -50,7 +50,8 @@ namespace {
 // 18 per row 23.0 and 21.9.
 constexpr int DQ_MANY = 32;
 constexpr int DQ_FEW = 4;            // at most this many: k_merge_few
-constexpr float DQ_PSHIFT = 15.f;  // weights are at most 2^15, fp16's largest number is 65504
+constexpr float DQ_PSHIFT = 15.f;       // weights are at most 2^15, fp16's largest number is 65504
+constexpr float DQ_PUNIT = 0x1p-15f;    // sums leave the tiles without that factor
 constexpr float DQ_VMIN = 0x1p-126f;  // v_ref of a row without a tile: the smallest normal number
 // 16-token tiles in flight per warp (4 KB each at head_dim 128): about 192 KB per SM
 constexpr int dq_stages(int warps) { return warps > 8 ? 48 / warps : 6; }
@@ -347,11 +348,12 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
                     float *o = a.o_part + (slot * a.G + head) * D + 2 * g4;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * v_ref, acc[nt][mt][2 + i] * v_ref);
+                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * DQ_PUNIT * v_ref,
+                                                                               acc[nt][mt][2 + i] * DQ_PUNIT * v_ref);
                     if (g4 == 0) {
                         float *ml = a.ml_part + (slot * a.G + head) * 2;
-                        ml[0] = m_run[nt][i] - DQ_PSHIFT;  // what the weights are relative to
-                        ml[1] = v;
+                        ml[0] = m_run[nt][i];
+                        ml[1] = v * DQ_PUNIT;
                     }
                 }
             }
@@ -743,13 +745,14 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
             v += __shfl_xor_sync(FULL, v, 16);
             if (g4 == 0) {
                 s_ml[warp][head][0] = m_run[nt][i];
-                s_ml[warp][head][1] = v;
+                s_ml[warp][head][1] = v * DQ_PUNIT;
             }
             if (head < a.G && valid) {
                 float *o = s_o + (warp * a.G + head) * D + 2 * g4;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * v_ref, acc[nt][mt][2 + i] * v_ref);
+                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * DQ_PUNIT * v_ref,
+                                                                           acc[nt][mt][2 + i] * DQ_PUNIT * v_ref);
             }
         }
     __syncthreads();
@@ -773,8 +776,7 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const size_t at = (size_t)b * a.Hq + (size_t)h * a.G + head;
         *reinterpret_cast<uint32_t *>(a.out + at * D + dim) = pack_bf16x2(o.x * inv, o.y * inv);
-        // the weights were relative to 2^-DQ_PSHIFT of the maximum
-        if (a.lse && dim == 0) a.lse[at] = l > 0.f ? (M - DQ_PSHIFT + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.lse && dim == 0) a.lse[at] = l > 0.f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
 }
 

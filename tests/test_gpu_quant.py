@@ -158,6 +158,22 @@ def test_decode_query_range_and_scale(fmt):
     check_attention(out, lse, want)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("exponent", [-110, 112])
+def test_decode_values_near_the_ends_of_the_range(fmt, exponent):
+    """Value scales that put the output near fp32's largest and smallest normal numbers; short and long rows."""
+    c = Case(fmt, [90, 7, 1500], 4, 2, 64, 16, seed=8).fill()
+    c.vs[:] = np.where(np.isnan(c.vs), c.vs, 2.0 ** exponent)
+    q, sel = c.queries(), c.select(94)
+    want = ref.attend(q.double().numpy(), *c.float_values(), c.ptr, c.idx, c.L, sel, 1 / 8)
+    cache = c.cache()
+    for splits in (0, 5):
+        out, lse = decode(c, cache, q.to(DEV), dev(sel), num_splits=splits)
+        check_attention(out, lse, want)
+    out, lse = decode(c, cache, q.to(DEV), dev(sel[:, :, :6]))
+    check_attention(out, lse, ref.attend(q.double().numpy(), *c.float_values(), c.ptr, c.idx, c.L, sel[:, :, :6], 1 / 8))
+
+
 def test_decode_late_pieces():
     """A share of 64 tiles or more per warp takes the split with late pieces: all of them equal one by one splits."""
     c = Case("e4m3", [32768] * 40, 8, 4, 64, 64, seed=2, pool=64)
