@@ -351,9 +351,10 @@ vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, co
 /*
  * vx_sparse_decode over an 8-bit cache: the same arguments, selection, workspace and results,
  * with K = k_code * k_scale and V = v_code * v_scale of each page and KV head.  The planned split
- * (num_splits 0) is its own: short rows (at most 32 tiles of 16 selected tokens), when there are
- * no more rows than SMs, go to one block each; otherwise vx_sparse_decode's rule for 16 warps per
- * SM (8 with more than 8 query heads per KV head).  Results never depend on timing.
+ * (num_splits 0) is its own: short rows (at most 32 tiles of 16 selected tokens), when their
+ * blocks all fit the GPU at once, go to one block each; otherwise chunks of an even number of
+ * tiles, dealt out over the SMs' 16 warps (8 with more than 8 query heads per KV head).  Results
+ * never depend on timing.
  * q and out stay bf16; logits, softmax statistics and sums are fp32.  Scales are any finite
  * fp32 numbers (vx_quant_update makes powers of two).
  */

@@ -275,7 +275,7 @@ WsLayout ws_layout(const vx_geometry *g, int32_t max_pages, int32_t k, const Pla
 // bytes vx_sparse_decode uses: the split partials (the start of the layout)
 size_t decode_ws_bytes(const WsLayout &l) { return l.scores; }
 
-// the 8-bit decode's plan: the same split rule for its own count of warps
+// The 8-bit decode's plan: plan() for its own count of warps and with its own rule for chunks.
 // Planned, short rows, and no more of them than fit the GPU at once: a block per row, whose warps join
 // their partials in shared memory, instead of a split over the GPU and a merge kernel.  Measured,
 // split and row (us): 32 rows of 8 tiles 7.9 and 4.4, 128 of 32 10.8 and 8.1, 256 of 16 10.3 and 7.3,
