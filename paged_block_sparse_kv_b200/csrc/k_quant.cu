@@ -18,11 +18,12 @@
 //  * Append: a warp per unit; the one new row, and for the centroid the page's key codes in
 //    16-byte chunks.  Value codes are read only when the scale grows.  Latency bound (length ->
 //    table -> codes).
-// Measured on one B200: prefill of 8 requests, 16-token pages, head_dim 128 (833 MB): e4m3 139 us, int8
-// 144 us, 5.8-6.0 TB/s (0.89-0.92 of the copy peak); 64-token pages 154 us; head_dim 64 0.58-0.66 of it
-// (a unit is half as long and its fixed part the same).  Four blocks per SM (64 registers): three
+// Measured on one B200: prefill of 8 ragged requests, 16-token pages, head_dim 128, e4m3 (833 MB): 144 us
+// warm and alone (0.88 of the copy peak), 150 in turn with other work (0.85).  Shortest of four graph
+// replays, which flatters: e4m3 139 us, int8 144, 64-token pages 154; head_dim 64 0.58-0.66 of the copy
+// peak (a unit is half as long and its fixed part the same).  Four blocks per SM (64 registers): three
 // took 156 us where four took 147 and two 174.  A grid of requests by pages, whose blocks past a short
-// request's end do nothing, took 148 us for the 8 ragged requests (and 486 where this one takes 507 for
+// request's end do nothing, took 151 us where this list takes 144 (and 486 where this one takes 507 for
 // 256 of equal length).  Append of 256 requests, 8 KV heads 5.6 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
