@@ -235,7 +235,7 @@ vx_status vx_compact_pages(const vx_geometry *geo, const vx_page_pool *pool, con
         return bad(VX_ERR_INVALID_ARG, "the pool must have num_pool_pages pages");
     VX_TRY(vx::validate_ptr(ref_in, "ref_in", false));
     VX_TRY(check_word_ptr(page_indices_out, "page_indices_out"));
-    VX_TRY(check_word_ptr(ref_out, "ref_out"));
+    VX_TRY(vx::validate_ptr(ref_out, "ref_out", false));  // written in 16-byte stores
     VX_TRY(check_word_ptr(remap, "remap"));
     VX_TRY(check_word_ptr(num_live, "num_live"));
     VX_TRY(check_word_ptr(err, "err", true));

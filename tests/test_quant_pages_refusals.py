@@ -1,0 +1,46 @@
+"""More refusals of the page and 8-bit cache calls, on the host: validation runs before any launch, so nothing here needs a
+GPU.  Pointers are made-up addresses that nothing dereferences."""
+import ctypes
+import os
+
+import pytest
+
+from paged_block_sparse_kv_b200 import vx
+
+FAKE, FAR = 4096, 1 << 40
+INVALID = vx.VX_ERR_INVALID_ARG
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(vx.LIB_PATH):
+        pytest.skip("libvx.so not built")
+    return vx.lib()
+
+
+def _geo(**kw):
+    g = dict(batch=2, num_q_heads=16, num_kv_heads=8, head_dim_qk=128, head_dim_v=128, page_size=16,
+             mla_shared_kv=0, num_pool_pages=5000)
+    g.update(kw)
+    return ctypes.byref(vx.vx_geometry(**g))
+
+
+def _table(max_pages=10, ptr=256):
+    return ctypes.byref(vx.vx_page_table(ptr, ptr, ptr, max_pages))
+
+
+def _pool(**kw):
+    p = dict(k_cache=1 << 30, v_cache=1 << 34, centroids=None, k_scale=None, v_scale=None, elem_bytes=2, num_pages=5000)
+    p.update(kw)
+    return ctypes.byref(vx.vx_page_pool(**p))
+
+
+@pytest.mark.parametrize("off", [4, 8, 12])
+@pytest.mark.parametrize("pages", [100, 5000])
+def test_compaction_counts_apart_and_misaligned(L, off, pages):
+    """ref_out is written in 16-byte stores when it is not ref_in: a row of a double buffer of odd length is refused."""
+    g = _geo(num_pool_pages=pages)
+    n = L.vx_page_workspace_size(g, 1)
+    assert L.vx_compact_pages(g, _pool(num_pages=pages), _table(), FAKE, FAKE, FAR + off, FAR + (1 << 20), FAKE, FAKE, n,
+                              None, None) == INVALID
+    assert b"ref_out" in L.vx_last_error()
