@@ -377,21 +377,25 @@ __device__ __noinline__ void quant_unit(bool go, bool is_key, int part, const __
     }
 }
 
+// Sums stop at 2^32 - 1: the lengths of a few requests may add up to more, and a sum that wrapped
+// would look small again.
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return a + min(b, ~a); }
+
 // Inclusive sum over the block; total: the block's sum.  s_part: QZ_WARPS words.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_part, uint32_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t y = __shfl_up_sync(FULL, v, off);
-        if (lane >= off) v += y;
+        if (lane >= off) v = sat_add(v, y);
     }
     if (lane == 31) s_part[warp] = v;
     __syncthreads();
     total = 0;
 #pragma unroll
     for (int w = 0; w < QZ_WARPS; ++w) {
-        if (w < warp) v += s_part[w];
-        total += s_part[w];
+        if (w < warp) v = sat_add(v, s_part[w]);
+        total = sat_add(total, s_part[w]);
     }
     __syncthreads();
     return v;
@@ -419,8 +423,8 @@ __global__ void __launch_bounds__(QZ_WARPS * 32, 4) k_quant_prefill(const Centro
         bool sound = b < a.B && L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L;
         const uint32_t n_new = sound ? L - fp : 0;
         uint32_t total;
-        const uint32_t end = rows + block_scan(n_new, s_part, total);
-        rows += total;
+        const uint32_t end = sat_add(rows, block_scan(n_new, s_part, total));
+        rows = sat_add(rows, total);
         sound = sound && end <= (uint64_t)qa.num_new;
         if (b < a.B && !sound && blockIdx.x == 0) set_err(a.err, VX_DATA_BAD_SEQ_LEN);
         const uint32_t n_pages = sound && L > fp ? ceil_div(L, a.P) - fp / a.P : 0;

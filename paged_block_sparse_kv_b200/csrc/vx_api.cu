@@ -834,6 +834,7 @@ vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, co
     if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
     if (num_new < 0 || (!first_pos && num_new < geo->batch))
         return fail(VX_ERR_INVALID_ARG, "num_new %lld rows: an append needs one per request", (long long)num_new);
+    if (num_new > INT32_MAX) return fail(VX_ERR_UNSUPPORTED, "num_new %lld: more than 2^31 - 1 rows", (long long)num_new);
     vx::QuantArgs qa = quant_args(cache);
     qa.num_new = num_new;
     cudaError_t e = vx::launch_quant_update(

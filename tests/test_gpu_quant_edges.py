@@ -1,0 +1,38 @@
+"""8-bit caches at the edges of their contract, against plain 64-bit implementations."""
+import numpy as np
+import pytest
+import torch
+
+import quant_ref as ref
+from paged_block_sparse_kv_b200 import vx
+from test_gpu_quant import DEV, FMTS, Case, check_cache, dev, new_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("over", [0, 1, 32])
+def test_lengths_that_add_up_to_more_than_32_bits(P, over):
+    """Two requests of almost 2^31 tokens bring more rows than there are, and so does every request behind them, although
+    the sum of the lengths, taken modulo 2^32, is small again: nothing is written."""
+    top = 2 ** 31 // P - 1
+    huge = top * P  # P tokens short of 2^31, so the two are 2 P short of 2^32
+    last = (2 * P + over, 20)
+    c = Case("int8", [P, P, *last], 2, 2, 64, P, seed=3).blank()
+    cache, cen = c.cache(), torch.zeros(c.pool, 2, 64, dtype=torch.bfloat16, device=DEV)
+    x = new_rows(c, 70).to(DEV)
+    t = vx.PageTable(c.table.page_ptr, c.table.page_indices, dev(np.array([huge, huge, *last])), top)
+    vx.vx_quant_update(c.geo, t, cache, cen, x, x, first_pos=dev(np.zeros(4)), err=c.err)
+    check_cache(c, cache, cen, np.zeros((c.pool, 2, 64)))
+    assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN
+    # the same behind a request that fits: that one is written
+    c = Case("int8", [30, P, P, *last], 2, 2, 64, P, seed=4).blank()
+    cache, cen = c.cache(), torch.zeros(c.pool, 2, 64, dtype=torch.bfloat16, device=DEV)
+    t = vx.PageTable(c.table.page_ptr, c.table.page_indices, dev(np.array([30, huge, huge, *last])), top)
+    c.err.zero_()
+    vx.vx_quant_update(c.geo, t, cache, cen, x, x, first_pos=dev(np.zeros(5)), err=c.err)
+    want = np.zeros((c.pool, 2, 64))
+    for a, s, w in ((c.k, c.ks, want), (c.v, c.vs, None)):
+        ref.quant_update(a, s, w, x.double().cpu().numpy(), c.ptr, c.idx, [30], [0], "int8")
+    check_cache(c, cache, cen, want)
+    assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN

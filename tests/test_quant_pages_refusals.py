@@ -44,3 +44,8 @@ def test_compaction_counts_apart_and_misaligned(L, off, pages):
     assert L.vx_compact_pages(g, _pool(num_pages=pages), _table(), FAKE, FAKE, FAR + off, FAR + (1 << 20), FAKE, FAKE, n,
                               None, None) == INVALID
     assert b"ref_out" in L.vx_last_error()
+
+
+def test_more_new_rows_than_31_bits(L):
+    c = ctypes.byref(vx.vx_quant_cache(vx.VX_QUANT_INT8, FAKE, FAKE, FAKE, FAKE))
+    assert L.vx_quant_update(_geo(), _table(), c, FAKE, FAKE, FAKE, 1 << 31, FAKE, None, None) == vx.VX_ERR_UNSUPPORTED
