@@ -150,6 +150,13 @@ __global__ void k_centroid_append(CentroidArgs a) {
                      static_cast<__nv_bfloat16 *>(a.centroids) + blk * D, lane);
 }
 
+// New tokens request i writes in a prefill: seq_lens[i] - first_pos[i], or none for a request
+// whose length or first position is out of range (reported by its own blocks).
+__device__ __forceinline__ int64_t prefill_count(const CentroidArgs &a, int i) {
+    const int32_t L = a.seq_lens[i], fp = a.first_pos[i];
+    return (L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L) ? (int64_t)(L - fp) : 0;
+}
+
 // One (page, head) of a prefill: rows [first_new, m) come from the packed input (new_row(t))
 // and are stored into the page, rows [0, first_new) are the page's older tokens; the fp64
 // sum of all m rows gives the centroid, as in centroid_warp.  New rows are loaded in groups

@@ -135,13 +135,6 @@ struct PageArgs {
     int32_t *head, *list_a, *list_b, *list_c, *list_d, *list_e, *list_f;
 };
 
-// New tokens request i writes in a prefill: seq_lens[i] - first_pos[i], or none for a request
-// whose length or first position is out of range (reported by its own blocks).
-__device__ __forceinline__ int64_t prefill_count(const CentroidArgs &a, int i) {
-    const int32_t L = a.seq_lens[i], fp = a.first_pos[i];
-    return (L >= 1 && L <= a.max_pages * a.P && fp >= 0 && fp <= L) ? (int64_t)(L - fp) : 0;
-}
-
 // One decode work unit (a 16-token tile of a selected page) after its metadata has been
 // looked up: row, tensor-map page(-head) index, token offset in the page, valid tokens.
 struct Resolved {
