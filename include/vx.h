@@ -331,7 +331,8 @@ vx_status vx_sparse_decode_noalloc(const vx_geometry *geo, const vx_page_table *
  * down to its subnormals, at most half a step of the new scale for int8).  A scale found in a
  * partly filled page may be any positive number (another program's): it is kept while it is
  * large enough.
- * code = x / s rounded to nearest, ties to even (s another program's: x * (1 / s)).
+ * code = x / s rounded to nearest, ties to even (s another program's: the fp32 product
+ * x * (1 / s) rounded, in an append and a prefill write alike).
  * Powers of two cost an int8 page up to one bit of its range (the mean is half a bit) and
  * make every step reproducible: division by s is exact, so the code of a value depends on
  * nothing but the value and s.

@@ -530,10 +530,13 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) k_quant_append(const CentroidAr
     bf16x8_to_f32(x[0], reinterpret_cast<float(&)[8]>(f));
     bf16x8_to_f32(x[1], reinterpret_cast<float(&)[8]>(f[8]));
     uint32_t c[4], bits[4];
+    // the product is rounded to fp32 before it is rounded to a code, as in quant_unit: under a scale that
+    // is no power of two one rounding less gives other int8 codes (9 of 4 million random values)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = four_codes<FMT>(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3], inv, bits);
+    for (int e = 0; e < 16; ++e) f[e] = __fmul_rn(f[e], inv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = four_codes<FMT>(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3], 1.f, bits);
     if (slot > 0 && s > s_old) {  // the older codes in the new scale
-        if (!is_key) load_old();
         const float ratio = s_old / s;
 #pragma unroll 1
         for (int i = 0; i < NR; ++i) {

@@ -36,3 +36,39 @@ def test_lengths_that_add_up_to_more_than_32_bits(P, over):
         ref.quant_update(a, s, w, x.double().cpu().numpy(), c.ptr, c.idx, [30], [0], "int8")
     check_cache(c, cache, cen, want)
     assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN
+
+
+def bf16_grid(lo, hi):
+    """Every positive bf16 number in [lo, hi)."""
+    a, b = (np.array([v], np.float32).view(np.uint32)[0] >> 16 for v in (lo, hi))
+    return (np.arange(a, b, dtype=np.uint32) << 16).view(np.float32)
+
+
+def test_int8_codes_under_an_odd_scale_are_the_same_in_an_append_and_a_prefill():
+    """Values whose fp32 product with 1 / s rounds onto a tie of two codes that the exact product lies beside."""
+    rng, D, P, B = np.random.default_rng(5), 64, 16, 40
+    scales, rows = [], []
+    x = bf16_grid(0.5, 90.0)
+    while len(scales) < B:
+        s = rng.uniform(0.75, 1.25, 1).astype(np.float32)[0]
+        inv = np.float32(1) / s
+        y = x * inv
+        split = x[(np.rint(y) != np.rint(x.astype(np.float64) * np.float64(inv))) & (y < 127)]
+        if len(split):
+            scales.append(s)
+            rows.append(np.where(rng.random(D) < 0.5, -1, 1) * rng.choice(np.concatenate([split, split, x[:400]]), D))
+    scales, rows = np.array(scales, np.float32), np.array(rows, np.float32)
+    got = []
+    for prefill in (False, True):
+        c = Case("int8", [2] * B, 1, 1, D, P, seed=6).fill()
+        first = c.idx[c.ptr]
+        c.ks[first, 0] = c.vs[first, 0] = scales
+        cache, cen = c.cache(), torch.zeros(c.pool, 1, D, dtype=torch.bfloat16, device=DEV)
+        new = torch.from_numpy(rows)[:, None].to(torch.bfloat16).to(DEV)
+        vx.vx_quant_update(c.geo, c.table, cache, cen, new, new, first_pos=dev(np.ones(B)) if prefill else None, err=c.err)
+        assert int(c.err.item()) == 0
+        assert np.array_equal(cache.k_scale.cpu().numpy(), c.ks, equal_nan=True)
+        got += [a.cpu().numpy()[first, 0, 1] for a in (cache.k_cache, cache.v_cache)]
+    want = np.rint(rows * (np.float32(1) / scales)[:, None])
+    for g in got:
+        assert np.array_equal(g, want)
