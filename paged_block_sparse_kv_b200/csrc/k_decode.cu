@@ -396,7 +396,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
 // launcher picks PER = 1 (more warps, for few rows with many partials) or a wider slice
 // (fewer warps: for many rows with few partials, or when the narrow shape would not fit in
 // one wave of resident warps).
-template <int DV, int PER, int GROUP>
+// NORMALISED (the 8-bit decode's partials): outputs are already divided by their own sum.  Their
+// weights are then the partials' shares of the total, so that nothing grows past the largest value.
+template <int DV, int PER, int GROUP, bool NORMALISED>
 __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
     pdl_wait();
     // the next grid on the stream may land now: the decode step's last kernel is short, and a
@@ -448,7 +450,9 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(FULL, lsum, off);
     // lane i keeps the weight of partial i of the first group
-    const float w_first = (M == -INFINITY || m_first == -INFINITY) ? 0.f : exp2f(m_first - M);
+    const float share = NORMALISED && lsum > 0.f ? 1.f / lsum : 1.f;
+    float w_first = (M == -INFINITY || m_first == -INFINITY) ? 0.f : exp2f(m_first - M);
+    if constexpr (NORMALISED) w_first *= l_first * share;
 
     float o[PER];
 #pragma unroll
@@ -469,14 +473,16 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
             // lane u < GROUP computes the weight of partial g0 + u
             const int i = g0 + lane;
             const float m = (lane < GROUP && i < np) ? ml0[(int64_t)i * a.G * 2] : -INFINITY;
-            const float w_lane = m == -INFINITY ? 0.f : exp2f(m - M);
+            float w_lane = m == -INFINITY ? 0.f : exp2f(m - M);
+            if constexpr (NORMALISED)
+                if (m != -INFINITY) w_lane *= ml0[(int64_t)i * a.G * 2 + 1] * share;
 #pragma unroll
             for (int u = 0; u < GROUP; ++u) add(v[u], __shfl_sync(FULL, w_lane, u));
         }
     }
     const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
     const size_t head = (size_t)b * a.Hq + (size_t)h * a.G + g;
-    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    const float inv = NORMALISED ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
     __nv_bfloat16 *dst = a.out + head * DV + slice * SLICE + lane * PER;
     if constexpr (PER == 1) {
         *dst = __float2bfloat16_rn(o[0] * inv);
@@ -512,7 +518,7 @@ cudaError_t launch_decode_gqa(const DecodeArgs &a, const CUtensorMap &tmK, const
     return cudaErrorInvalidValue;
 }
 
-template <int DV>
+template <int DV, bool NORMALISED>
 static cudaError_t launch_merge_dv(const DecodeArgs &a, cudaStream_t s, bool pdl) {
     constexpr int PW = DV >= 128 ? 4 : 2;  // dims per lane of the wide shape
     int dev = 0, sms = 0;
@@ -535,18 +541,26 @@ static cudaError_t launch_merge_dv(const DecodeArgs &a, cudaStream_t s, bool pdl
     // 74.6 us per step; long context, ~20 partials per row, is faster narrow: 67.6 vs 68.0)
     if (np_max <= 8 || wide_items >= (int64_t)sms * 8 * 4 || narrow_items > narrow_resident) {
         const dim3 grid((unsigned)((wide_items + 7) / 8));
-        return launch_k(k_merge<DV, PW, 32 / PW>, grid, dim3(256), 0, s, pdl, a);
+        return launch_k(k_merge<DV, PW, 32 / PW, NORMALISED>, grid, dim3(256), 0, s, pdl, a);
     }
     const dim3 grid((unsigned)((narrow_items + 7) / 8));
-    if (np_max <= 16) return launch_k(k_merge<DV, 1, 16>, grid, dim3(256), 0, s, pdl, a);
-    return launch_k(k_merge<DV, 1, 32>, grid, dim3(256), 0, s, pdl, a);
+    if (np_max <= 16) return launch_k(k_merge<DV, 1, 16, NORMALISED>, grid, dim3(256), 0, s, pdl, a);
+    return launch_k(k_merge<DV, 1, 32, NORMALISED>, grid, dim3(256), 0, s, pdl, a);
 }
 
 cudaError_t launch_merge(const DecodeArgs &a, cudaStream_t s, bool pdl) {
     switch (a.Dv) {
-        case 64: return launch_merge_dv<64>(a, s, pdl);
-        case 128: return launch_merge_dv<128>(a, s, pdl);
-        case 512: return launch_merge_dv<512>(a, s, pdl);
+        case 64: return launch_merge_dv<64, false>(a, s, pdl);
+        case 128: return launch_merge_dv<128, false>(a, s, pdl);
+        case 512: return launch_merge_dv<512, false>(a, s, pdl);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_merge_normalised(const DecodeArgs &a, cudaStream_t s, bool pdl) {
+    switch (a.Dv) {
+        case 64: return launch_merge_dv<64, true>(a, s, pdl);
+        case 128: return launch_merge_dv<128, true>(a, s, pdl);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,7 +3,9 @@
 // For query head g of KV head h, over the valid tokens t of the selected pages p:
 //   x_t = sm_scale * k_scale[p][h] * (q_g . kc_t),  out = sum_t softmax(x)_t v_scale[p][h] vc_t
 // with kc, vc the codes (int8 or e4m3).  The work split (flat list of 16-token tiles, pieces,
-// one partial per (row, piece), merge) is that of k_decode.cu, whose merge kernel is used.
+// one partial per (row, piece), merge) is that of k_decode.cu, and so is a merge kernel.  Partials
+// are divided by their own sums here: a sum of weighted values, undivided, leaves fp32's range when
+// the values are near its end (a thousand of 2^119 do), their mean does not.
 //
 // Both code types are exact in fp16 (int8: integers up to 128; e4m3: 4 significant bits,
 // 2^-9 .. 448), so the products run as fp16 mma with fp32 sums and the scales stay outside:
@@ -332,7 +334,8 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     float m_run[NT][2], l_run[NT][2];
     float v_ref = DQ_VMIN, v_inv = 1.f / DQ_VMIN;
 
-    // partial of row `r` (at least one tile attended) for piece `c`: slot r + c
+    // partial of row `r` (at least one tile attended) for piece `c`: slot r + c.  The output is divided
+    // by its sum before v_ref goes in: no number is then larger than the largest value
     auto write_partial = [&](int64_t r, int64_t c) {
         const int64_t slot = r + c;
 #pragma unroll
@@ -346,10 +349,11 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
                 v += __shfl_xor_sync(FULL, v, 16);
                 if (head < a.G) {
                     float *o = a.o_part + (slot * a.G + head) * D + 2 * g4;
+                    const float inv = v > 0.f ? 1.f / v : 0.f;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * DQ_PUNIT * v_ref,
-                                                                               acc[nt][mt][2 + i] * DQ_PUNIT * v_ref);
+                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * v_ref,
+                                                                               acc[nt][mt][2 + i] * inv * v_ref);
                     if (g4 == 0) {
                         float *ml = a.ml_part + (slot * a.G + head) * 2;
                         ml[0] = m_run[nt][i];
@@ -522,8 +526,8 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     }
 }
 
-// Partials (unnormalised output, maximum in log2 units, sum) of one row and query head, joined in
-// order by a warp; D / 32 dims per lane.
+// Partials (output, maximum in log2 units, sum) of one row and query head, joined in order by a warp;
+// D / 32 dims per lane.  Outputs are divided by their sums, here as in the partials.
 template <int D>
 struct Joined {
     static constexpr int PER = D / 32;
@@ -534,33 +538,47 @@ struct Joined {
 #pragma unroll
         for (int d = 0; d < PER; ++d) o[d] = 0.f;
     }
-    // n partials, `stride` heads apart: the maximum of all first, then the weighted sums; an empty
-    // one (maximum -inf) left no output
+    // n partials, `stride` heads apart: the maximum of all and the sum first, then the outputs by their
+    // shares of it; an empty one (maximum -inf) left no output.  Lane i reads partial i's maximum and
+    // sum, and the first 8 outputs are on their way meanwhile.
     __device__ __forceinline__ void add_all(const float *op, const float *ml, int64_t stride, int n, int lane) {
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i * stride * 2]);
+        auto pair = [&](int i) {
+            return i < n ? make_float2(ml[i * stride * 2], ml[i * stride * 2 + 1]) : make_float2(-INFINITY, 0.f);
+        };
+        auto load = [&](Vec (&v)[8], int i0) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = *reinterpret_cast<const Vec *>(op + min(i0 + u, n - 1) * stride * D + lane * PER);
+        };
+        Vec v[8];
+        load(v, 0);
+        const float2 first = pair(lane);
+        m = first.x;
+        for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, ml[i * stride * 2]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
         if (m == -INFINITY) return;
+        auto weight = [&](float2 x) { return x.x == -INFINITY ? 0.f : exp2f(x.x - m) * x.y; };
+        float w = weight(first);
+        l = w;
+        for (int i = lane + 32; i < n; i += 32) l += weight(pair(i));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(FULL, l, off);
+        const float share = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            Vec v[8];
-            float w[8], li[8];
+        for (int i0 = 0;;) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int i = min(i0 + u, n - 1);
-                v[u] = *reinterpret_cast<const Vec *>(op + i * stride * D + lane * PER);
-                w[u] = ml[i * stride * 2];
-                li[u] = ml[i * stride * 2 + 1];
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (i0 + u >= n || w[u] == -INFINITY) continue;
-                const float f = exp2f(w[u] - m);
+                const float f = __shfl_sync(FULL, w, u) * share;
                 const float *x = reinterpret_cast<const float *>(&v[u]);
-                l += f * li[u];
+                if (f != 0.f) {
 #pragma unroll
-                for (int d = 0; d < PER; ++d) o[d] += f * x[d];
+                    for (int d = 0; d < PER; ++d) o[d] += f * x[d];
+                }
             }
+            if ((i0 += 8) >= n) break;
+            load(v, i0);
+            w = weight(pair(i0 + lane));
         }
     }
     __device__ __forceinline__ void store(float *op, float *ml, int lane) const {
@@ -573,10 +591,9 @@ struct Joined {
     __device__ __forceinline__ void finish(const DecodeArgs &a, int64_t r, int g, int lane) const {
         const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
         const size_t head = (size_t)b * a.Hq + (size_t)h * a.G + g;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + head * D + lane * PER);
 #pragma unroll
-        for (int d = 0; d < PER; d += 2) dst[d / 2] = pack_bf16x2(o[d] * inv, o[d + 1] * inv);
+        for (int d = 0; d < PER; d += 2) dst[d / 2] = pack_bf16x2(o[d], o[d + 1]);
         if (a.lse && lane == 0) a.lse[head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
 };
@@ -634,12 +651,18 @@ __global__ void __launch_bounds__(256, 6) k_merge_few(const DecodeArgs a) {
     J j;
 #pragma unroll
     for (int i = 0; i < DQ_FEW; ++i) j.m = fmaxf(j.m, s[i].x);
+    float w[DQ_FEW];
+#pragma unroll
+    for (int i = 0; i < DQ_FEW; ++i) {
+        w[i] = s[i].x == -INFINITY ? 0.f : exp2f(s[i].x - j.m) * s[i].y;
+        j.l += w[i];
+    }
+    const float share = j.l > 0.f ? 1.f / j.l : 0.f;
 #pragma unroll
     for (int i = 0; i < DQ_FEW; ++i) {
         if (s[i].x == -INFINITY) continue;  // an empty partial left no output
-        const float f = exp2f(s[i].x - j.m);
+        const float f = w[i] * share;
         const float *x = reinterpret_cast<const float *>(&v[i]);
-        j.l += f * s[i].y;
 #pragma unroll
         for (int d = 0; d < J::PER; ++d) j.o[d] += f * x[d];
     }
@@ -747,12 +770,13 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
                 s_ml[warp][head][0] = m_run[nt][i];
                 s_ml[warp][head][1] = v * DQ_PUNIT;
             }
-            if (head < a.G && valid) {
+            if (head < a.G && valid) {  // divided by its sum, as in k_decode_quant
                 float *o = s_o + (warp * a.G + head) * D + 2 * g4;
+                const float inv = v > 0.f ? 1.f / v : 0.f;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * DQ_PUNIT * v_ref,
-                                                                           acc[nt][mt][2 + i] * DQ_PUNIT * v_ref);
+                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * v_ref,
+                                                                           acc[nt][mt][2 + i] * inv * v_ref);
             }
         }
     __syncthreads();
@@ -763,19 +787,23 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
         float2 o = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][head][0]);
-#pragma unroll 4
+        float f[WARPS];
+#pragma unroll
         for (int w = 0; w < WARPS; ++w) {
             const float m = s_ml[w][head][0];
-            if (m == -INFINITY) continue;
-            const float f = exp2f(m - M);
-            const float2 x = *reinterpret_cast<const float2 *>(s_o + (w * a.G + head) * D + dim);
-            l += f * s_ml[w][head][1];
-            o.x += f * x.x;
-            o.y += f * x.y;
+            f[w] = m == -INFINITY ? 0.f : exp2f(m - M) * s_ml[w][head][1];
+            l += f[w];
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float share = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (s_ml[w][head][0] == -INFINITY) continue;
+            const float2 x = *reinterpret_cast<const float2 *>(s_o + (w * a.G + head) * D + dim);
+            o.x += f[w] * share * x.x;
+            o.y += f[w] * share * x.y;
+        }
         const size_t at = (size_t)b * a.Hq + (size_t)h * a.G + head;
-        *reinterpret_cast<uint32_t *>(a.out + at * D + dim) = pack_bf16x2(o.x * inv, o.y * inv);
+        *reinterpret_cast<uint32_t *>(a.out + at * D + dim) = pack_bf16x2(o.x, o.y);
         if (a.lse && dim == 0) a.lse[at] = l > 0.f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
 }
@@ -818,7 +846,7 @@ cudaError_t launch_dnf(const DecodeArgs &a, const QuantArgs &qa, const CUtensorM
     if (late) most += div64(a.units_per_row * (a.chunks - a.static_chunks) + a.units - a.static_units - 1, a.units - a.static_units) + 1;
     if (most <= DQ_FEW)
         return launch_k(k_merge_few<D>, dim3((unsigned)((rows * a.G + 7) / 8)), dim3(256), 0, s, true, a);
-    return launch_merge(a, s, true);
+    return launch_merge_normalised(a, s, true);
 }
 
 template <int D, int NT>

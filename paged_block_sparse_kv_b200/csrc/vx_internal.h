@@ -197,6 +197,8 @@ cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_update_table(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_compact_pages(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_merge(const DecodeArgs &a, cudaStream_t s, bool pdl);
+// the same for partials that are divided by their own sum (8-bit decode)
+cudaError_t launch_merge_normalised(const DecodeArgs &a, cudaStream_t s, bool pdl);
 // grid = SM count (one block of FUSED_WARPS warps per SM)
 cudaError_t launch_fused(const FusedArgs &a, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t s);
 // shared memory the fused kernel needs for a batch of B (0 if it cannot run it)

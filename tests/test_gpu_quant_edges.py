@@ -5,7 +5,7 @@ import torch
 
 import quant_ref as ref
 from paged_block_sparse_kv_b200 import vx
-from test_gpu_quant import DEV, FMTS, Case, check_cache, dev, new_rows
+from test_gpu_quant import DEV, FMTS, Case, check_attention, check_cache, decode, dev, new_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,26 @@ def test_int8_codes_under_an_odd_scale_are_the_same_in_an_append_and_a_prefill()
     want = np.rint(rows * (np.float32(1) / scales)[:, None])
     for g in got:
         assert np.array_equal(g, want)
+
+
+@pytest.mark.parametrize("fmt,code,exponent", [("int8", 127, 121), ("int8", -127, 100), ("e4m3", 448, 119), ("e4m3", -448, 112)])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+def test_values_of_one_sign_at_the_end_of_the_range(fmt, code, exponent, D, P):
+    """Every value is the same large number, up to bf16's largest: so is every output, however the row is split, though the
+    sum of the weighted values before its division by the sum of the weights is far outside fp32's range."""
+    c = Case(fmt, [P, 6 * P + 3, 200 * P - 1], 4, 2, D, P, seed=17).fill()
+    for b, n in enumerate(c.L):
+        for j in range(-(-int(n) // P)):
+            c.v[c.idx[c.ptr[b] + j], :, :min(P, int(n) - j * P)] = ref.nearest(np.array([float(code)]), fmt)[0]
+    c.vs[:] = 2.0 ** exponent
+    q, cache = c.queries(0.25), c.cache()
+    for k in (6, 30, 200):  # a block per row; few partials; many
+        sel = c.select(k)
+        value = code * 2.0 ** exponent
+        for splits in (0, 1, 3, 24, 100000):
+            out, lse = decode(c, cache, q.to(DEV), dev(sel), num_splits=splits)
+            # weights sum to one up to their roundings: fp16 weights (2^-11), the merge's (2^-18), and out's own to bf16
+            rel = (out.double() / value - 1).abs()
+            assert bool(torch.isfinite(out).all()) and float(rel.max()) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18, (k, splits)
+            assert bool(torch.isfinite(lse).all())
+    assert int(c.err.item()) == 0
