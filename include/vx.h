@@ -357,7 +357,9 @@ vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, co
  * tiles, dealt out over the SMs' 16 warps (8 with more than 8 query heads per KV head).  Results
  * never depend on timing.
  * q and out stay bf16; logits, softmax statistics and sums are fp32.  Scales are any finite
- * fp32 numbers (vx_quant_update makes powers of two).
+ * fp32 numbers (vx_quant_update makes powers of two), a row's pages may differ in them by any
+ * factor.  A weight times its page's v_scale is rounded to fp16's 11 bits, and to at most 2^-35 of
+ * the row's largest such product.
  */
 vx_status vx_sparse_decode_quant(const vx_geometry *geo, const vx_page_table *table, const void *q,
                                  const vx_quant_cache *cache, const int32_t *sel, int32_t k, float sm_scale,

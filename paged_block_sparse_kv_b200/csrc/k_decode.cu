@@ -397,7 +397,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
 // (fewer warps: for many rows with few partials, or when the narrow shape would not fit in
 // one wave of resident warps).
 // NORMALISED (the 8-bit decode's partials): outputs are already divided by their own sum.  Their
-// weights are then the partials' shares of the total, so that nothing grows past the largest value.
+// weights are then the partials' shares of the total, so that nothing grows past the largest value,
+// and a weight is multiplied in as two factors, so that one below fp32's smallest number still counts
+// beside a large output.
 template <int DV, int PER, int GROUP, bool NORMALISED>
 __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
     pdl_wait();
@@ -451,21 +453,29 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
     for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(FULL, lsum, off);
     // lane i keeps the weight of partial i of the first group
     const float share = NORMALISED && lsum > 0.f ? 1.f / lsum : 1.f;
-    float w_first = (M == -INFINITY || m_first == -INFINITY) ? 0.f : exp2f(m_first - M);
-    if constexpr (NORMALISED) w_first *= l_first * share;
+    auto weight = [&](float m) {  // NORMALISED: its root
+        return (M == -INFINITY || m == -INFINITY) ? 0.f : exp2f(NORMALISED ? 0.5f * (m - M) : m - M);
+    };
+    const float w_first = weight(m_first), part_first = w_first * l_first * share;
 
     float o[PER];
 #pragma unroll
     for (int d = 0; d < PER; ++d) o[d] = 0.f;
     // an empty partial (max -inf) holds no output values: read, then dropped
-    auto add = [&](const VecT &x, float w) {
+    auto add = [&](const VecT &x, float w, float part) {
         const float *xv = reinterpret_cast<const float *>(&x);
 #pragma unroll
-        for (int d = 0; d < PER; ++d) o[d] += w != 0.f ? w * xv[d] : 0.f;
+        for (int d = 0; d < PER; ++d) {
+            if constexpr (NORMALISED) o[d] += w != 0.f ? xv[d] * w * part : 0.f;
+            else o[d] += w != 0.f ? w * xv[d] : 0.f;
+        }
+    };
+    auto lane_of = [&](float w_lane, float part_lane, int u, const VecT &x) {
+        add(x, __shfl_sync(FULL, w_lane, u), NORMALISED ? __shfl_sync(FULL, part_lane, u) : 0.f);
     };
     if (M != -INFINITY) {
 #pragma unroll
-        for (int u = 0; u < GROUP; ++u) add(v[u], __shfl_sync(FULL, w_first, u));
+        for (int u = 0; u < GROUP; ++u) lane_of(w_first, part_first, u, v[u]);
 #pragma unroll 1
         for (int g0 = GROUP; g0 < np; g0 += GROUP) {  // rows with more than GROUP partials
 #pragma unroll
@@ -473,11 +483,12 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
             // lane u < GROUP computes the weight of partial g0 + u
             const int i = g0 + lane;
             const float m = (lane < GROUP && i < np) ? ml0[(int64_t)i * a.G * 2] : -INFINITY;
-            float w_lane = m == -INFINITY ? 0.f : exp2f(m - M);
+            const float w_lane = weight(m);
+            float part_lane = 0.f;
             if constexpr (NORMALISED)
-                if (m != -INFINITY) w_lane *= ml0[(int64_t)i * a.G * 2 + 1] * share;
+                if (m != -INFINITY) part_lane = w_lane * ml0[(int64_t)i * a.G * 2 + 1] * share;
 #pragma unroll
-            for (int u = 0; u < GROUP; ++u) add(v[u], __shfl_sync(FULL, w_lane, u));
+            for (int u = 0; u < GROUP; ++u) lane_of(w_lane, part_lane, u, v[u]);
         }
     }
     const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);

@@ -14,7 +14,8 @@
 // element into [2^14, 2^15), exact for every element down to 2^-29 of the largest (smaller
 // ones keep an absolute error of 2^-40 of it), and the factor goes into the logits' scale.  P
 // is rounded to fp16, to half a step of 2^-10 where bf16's is 2^-7; it is taken relative to
-// 2^-DQ_PSHIFT of the running maximum, so that weights down to 2^-29 are normal numbers.
+// 2^-DQ_PSHIFT of the running maximum of weight times v_scale, so that what is down to 2^-29 of it is
+// a normal number.
 //
 // Fragments straight from 8-bit tiles, no transposition of bytes:
 //  * K (A operand, tokens x dims): the order of the contracted dims is free as long as Q has
@@ -53,8 +54,8 @@ namespace {
 constexpr int DQ_MANY = 32;
 constexpr int DQ_FEW = 4;            // at most this many: k_merge_few
 constexpr float DQ_PSHIFT = 15.f;       // weights are at most 2^15, fp16's largest number is 65504
-constexpr float DQ_PUNIT = 0x1p-15f;    // sums leave the tiles without that factor
-constexpr float DQ_VMIN = 0x1p-126f;  // v_ref of a row without a tile: the smallest normal number
+constexpr float DQ_PUNIT = 0x1p-15f;    // the output leaves the tiles without that factor
+constexpr float DQ_MLAG = 16.f;         // the softmax's reference may stay this far below the largest logit (log2 units)
 // 16-token tiles in flight per warp (4 KB each at head_dim 128): about 192 KB per SM
 constexpr int dq_stages(int warps) { return warps > 8 ? 48 / warps : 6; }
 
@@ -124,19 +125,36 @@ struct Tile {
     float ks, vs;
 };
 
+// How the value scales of two tiles, and of a row's tiles so far, lie to one another.
+struct Spread {
+    float low = INFINITY;  // the smallest of the row
+
+    // with the next one or two tiles: may they go as a pair, and is `far` needed?
+    __device__ __forceinline__ void next(float a, float b, bool &pair, bool &far) {
+        const float lo = fminf(fabsf(a), fabsf(b)), hi = fmaxf(fabsf(a), fabsf(b));
+        low = fminf(low, lo);
+        far = !(hi <= low * 0x1p60f) || low < 0x1p-100f;
+        pair = hi <= lo * 16.f && !far;
+    }
+};
+
 // T 16-token tiles of one row.  qf: the query heads as mma B fragments in the dims order above; hs:
-// the logits' scale of heads 2 q4, 2 q4 + 1 (log2 units).  acc: the output, unnormalised, in units
-// of v_ref, the largest |v_scale| met so far: P is multiplied by v_scale / v_ref before it is
-// rounded, so acc needs no multiplication per tile; it is rescaled when the running maximum or
-// v_ref moves, which after a row's first tiles is rare.  (A page whose scale is below 2^-29 of
-// v_ref has its weights rounded as subnormal numbers: an error of at most 2^-40 of the largest
-// weight times v_ref.)  Two tiles at a time share the maximum's shuffles and give the scheduler
-// two independent chains.
+// the logits' scale of heads 2 q4, 2 q4 + 1 (log2 units).  Weights are exp2(logit - m_run) and l_run is
+// their sum; m_run stays up to DQ_MLAG behind the largest logit.  acc: the output, unnormalised, in
+// units of 2^(o_run - DQ_PSHIFT), where o_run is the largest logit + log2 of v_scale met: P is
+// multiplied by v_scale * unit, unit = 2^(m_run - o_run + DQ_PSHIFT), before it is rounded to fp16, so acc
+// needs no multiplication per tile.  What that rounding loses is at most 2^-35 of the largest weight
+// times v_scale met, whatever the scales of the row's pages are: in units of the largest v_scale alone,
+// all of a page was lost that carries the weight under a scale 2^-42 of another's.  (Of a pair, o_run
+// follows the larger scale: 4 bits of 2^-40, and the scale's rounding to a power of two one.)  far: a
+// weight or the unit may leave fp32's range, because the row's scales differ by more than 2^60 or one is
+// below 2^-100: then weight and scale share one exponent.  Two tiles at a time share the maximum's
+// shuffles and give the scheduler two independent chains.
 template <int D, int NT, int FMT, int T>
 __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32_t (&qf)[NT][D / 16][2],
                                              const float (&hs)[NT][2], float (&acc)[NT][D / 16][4],
-                                             float (&m_run)[NT][2], float (&l_run)[NT][2], float &v_ref, float &v_inv,
-                                             int lane) {
+                                             float (&m_run)[NT][2], float (&l_run)[NT][2], float (&o_run)[NT][2],
+                                             float (&unit)[NT][2], bool far, int lane) {
     constexpr int MT = D / 16;
     constexpr int HALVES = D / 64;  // 16-byte chunks a lane takes of a token row
     const int g4 = lane >> 2, q4 = lane & 3;
@@ -166,23 +184,17 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
             }
         }
     }
-    // v_ref of these tiles
-    float v_top = v_ref;
+    // 2^(ve - 1) < |v_scale| <= 2^ve of the tile with the largest
+    float vs_top = fabsf(tile[0].vs);
 #pragma unroll
-    for (int t = 0; t < T; ++t) v_top = fmaxf(v_top, fabsf(tile[t].vs));
-    float v_alpha = 1.f;
-    if (v_top > v_ref) {
-        v_alpha = v_ref / v_top;
-        v_ref = v_top;
-        v_inv = 1.f / v_top;
-    }
+    for (int t = 1; t < T; ++t) vs_top = fmaxf(vs_top, fabsf(tile[t].vs));
+    const float ve = __uint_as_float(0x4b000000u + ((__float_as_uint(vs_top) + 0x7fffffu) >> 23)) - 8388735.f;
     // online softmax (base 2), tokens >= nvalid masked
     uint32_t pb[T][NT][2];
-    float alpha[NT][2];
-    bool moved = v_alpha != 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float x[T][4];
+        float x[T][4], m_new[2], o_new[2];
+        bool change = false;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             const float f[2] = {hs[nt][0] * tile[t].ks, hs[nt][1] * tile[t].ks};
@@ -198,33 +210,46 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-            const float m_new = fmaxf(m_run[nt][i], mx);
-            alpha[nt][i] = exp2f(m_run[nt][i] - m_new);
-            moved |= alpha[nt][i] != 1.f;
-            m_run[nt][i] = m_new;
-            l_run[nt][i] *= alpha[nt][i];
-            alpha[nt][i] *= v_alpha;
+            const float top = mx + ve;
+            m_new[i] = mx > m_run[nt][i] + DQ_MLAG ? mx : m_run[nt][i];
+            o_new[i] = fmaxf(o_run[nt][i], top);
+            change |= mx > m_run[nt][i] + DQ_MLAG || top > o_run[nt][i];
         }
-        const float m0[2] = {m_run[nt][0] - DQ_PSHIFT, m_run[nt][1] - DQ_PSHIFT};
+        if (__any_sync(FULL, change)) {  // rare after a row's first tiles
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float alpha = exp2f(o_run[nt][i] - o_new[i]);
+                l_run[nt][i] *= exp2f(m_run[nt][i] - m_new[i]);
+                unit[nt][i] = exp2f(m_new[i] - o_new[i] + DQ_PSHIFT);
+                m_run[nt][i] = m_new[i];
+                o_run[nt][i] = o_new[i];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    acc[nt][mt][i] *= alpha;
+                    acc[nt][mt][i + 2] *= alpha;
+                }
+            }
+        }
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const float r = tile[t].vs * v_inv;
+            const float r[2] = {tile[t].vs * unit[nt][0], tile[t].vs * unit[nt][1]};
             float p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - m0[e & 1]);
+            for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - m_run[nt][e & 1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) l_run[nt][i] += p[i] + p[i + 2];
-            pb[t][nt][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0] * r, p[1] * r)));
-            pb[t][nt][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2] * r, p[3] * r)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] *= r[e & 1];
+            if (T == 1 && far) {
+                const uint32_t bits = __float_as_uint(tile[t].vs), field = (bits >> 23) & 0xffu;
+                const float mant = field ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : tile[t].vs * 0x1p126f;
+                const float by = static_cast<float>(static_cast<int>(max(field, 1u)) - 127) + DQ_PSHIFT;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - o_run[nt][e & 1] + by) * mant;
+            }
+            pb[t][nt][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
+            pb[t][nt][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
         }
-    }
-    if (__any_sync(FULL, moved)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][mt][e] *= alpha[nt][e & 1];
     }
     // O^T[dim][head] += codes . P^T
     const int mi = lane >> 3, tok = (lane & 7) + 8 * (mi & 1);
@@ -331,11 +356,10 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     uint32_t qf[NT][MT][2];
     float hs[NT][2];
     float acc[NT][MT][4];
-    float m_run[NT][2], l_run[NT][2];
-    float v_ref = DQ_VMIN, v_inv = 1.f / DQ_VMIN;
+    float m_run[NT][2], l_run[NT][2], o_run[NT][2], unit[NT][2];
 
     // partial of row `r` (at least one tile attended) for piece `c`: slot r + c.  The output is divided
-    // by its sum before v_ref goes in: no number is then larger than the largest value
+    // by its sum before its unit goes in: no number is then larger than the largest value
     auto write_partial = [&](int64_t r, int64_t c) {
         const int64_t slot = r + c;
 #pragma unroll
@@ -349,22 +373,23 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
                 v += __shfl_xor_sync(FULL, v, 16);
                 if (head < a.G) {
                     float *o = a.o_part + (slot * a.G + head) * D + 2 * g4;
-                    const float inv = v > 0.f ? 1.f / v : 0.f;
+                    const float inv = v > 0.f ? __fdividef(DQ_PUNIT, v) : 0.f;
+                    const float half = exp2f(0.5f * (o_run[nt][i] - m_run[nt][i]));  // the unit can be 2^128
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * v_ref,
-                                                                               acc[nt][mt][2 + i] * inv * v_ref);
+                        *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * half * half,
+                                                                               acc[nt][mt][2 + i] * inv * half * half);
                     if (g4 == 0) {
                         float *ml = a.ml_part + (slot * a.G + head) * 2;
                         ml[0] = m_run[nt][i];
-                        ml[1] = v * DQ_PUNIT;
+                        ml[1] = v;
                     }
                 }
             }
     };
+    Spread spread;
     auto start_row = [&](int64_t r) {
-        v_ref = DQ_VMIN;
-        v_inv = 1.f / DQ_VMIN;
+        spread = Spread();
         const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
         const __nv_bfloat16 *qb = a.q + ((size_t)b * a.Hq + (size_t)h * a.G) * D;
         load_query<D, NT>(qb, a.G, a.scale_log2, qf, hs, lane);
@@ -372,8 +397,8 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m_run[nt][i] = -INFINITY;
-                l_run[nt][i] = 0.f;
+                m_run[nt][i] = o_run[nt][i] = -INFINITY;
+                l_run[nt][i] = unit[nt][i] = 0.f;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -513,12 +538,16 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
             tile[k] = {at, at + TILE_BYTES, m.nvalid, m.ks, m.vs};
         };
         take(0, st);
+        tile[1] = tile[0];
         if (count == 2) take(1, st1);
+        bool pair, far;
+        spread.next(tile[0].vs, tile[1].vs, pair, far);
+        if (!pair) count = 1;  // the second one waits for the next round
         if (count == 2) {
-            attend_codes<D, NT, FMT, 2>(tile, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+            attend_codes<D, NT, FMT, 2>(tile, qf, hs, acc, m_run, l_run, o_run, unit, false, lane);
         } else {
             const Tile one[1] = {tile[0]};
-            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, o_run, unit, far, lane);
         }
         attended = true;
         __syncwarp();  // every lane is done with these stages before they are refilled
@@ -558,27 +587,35 @@ struct Joined {
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
         if (m == -INFINITY) return;
-        auto weight = [&](float2 x) { return x.x == -INFINITY ? 0.f : exp2f(x.x - m) * x.y; };
-        float w = weight(first);
-        l = w;
-        for (int i = lane + 32; i < n; i += 32) l += weight(pair(i));
+        // exp2(x - m) as a square: the product with a partial's output is taken in two steps, so that a weight
+        // below fp32's smallest number still counts beside a large output
+        auto root = [&](float x) { return x == -INFINITY ? 0.f : exp2f(0.5f * (x - m)); };
+        float h = root(first.x), hl = h * first.y;
+        l = h * hl;
+        for (int i = lane + 32; i < n; i += 32) {
+            const float2 x = pair(i);
+            const float r = root(x.x);
+            l += r * r * x.y;
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(FULL, l, off);
-        const float share = l > 0.f ? 1.f / l : 0.f;
+        const float share = l > 0.f ? __fdividef(1.f, l) : 0.f;
 #pragma unroll 1
         for (int i0 = 0;;) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const float f = __shfl_sync(FULL, w, u) * share;
+                const float f = __shfl_sync(FULL, h, u), g = __shfl_sync(FULL, hl, u) * share;
                 const float *x = reinterpret_cast<const float *>(&v[u]);
                 if (f != 0.f) {
 #pragma unroll
-                    for (int d = 0; d < PER; ++d) o[d] += f * x[d];
+                    for (int d = 0; d < PER; ++d) o[d] += x[d] * f * g;
                 }
             }
             if ((i0 += 8) >= n) break;
             load(v, i0);
-            w = weight(pair(i0 + lane));
+            const float2 x = pair(i0 + lane);
+            h = root(x.x);
+            hl = h * x.y;
         }
     }
     __device__ __forceinline__ void store(float *op, float *ml, int lane) const {
@@ -651,20 +688,20 @@ __global__ void __launch_bounds__(256, 6) k_merge_few(const DecodeArgs a) {
     J j;
 #pragma unroll
     for (int i = 0; i < DQ_FEW; ++i) j.m = fmaxf(j.m, s[i].x);
-    float w[DQ_FEW];
+    float h[DQ_FEW];  // as in Joined
 #pragma unroll
     for (int i = 0; i < DQ_FEW; ++i) {
-        w[i] = s[i].x == -INFINITY ? 0.f : exp2f(s[i].x - j.m) * s[i].y;
-        j.l += w[i];
+        h[i] = s[i].x == -INFINITY ? 0.f : exp2f(0.5f * (s[i].x - j.m));
+        j.l += h[i] * h[i] * s[i].y;
     }
-    const float share = j.l > 0.f ? 1.f / j.l : 0.f;
+    const float share = j.l > 0.f ? __fdividef(1.f, j.l) : 0.f;
 #pragma unroll
     for (int i = 0; i < DQ_FEW; ++i) {
         if (s[i].x == -INFINITY) continue;  // an empty partial left no output
-        const float f = w[i] * share;
+        const float f = h[i] * s[i].y * share;
         const float *x = reinterpret_cast<const float *>(&v[i]);
 #pragma unroll
-        for (int d = 0; d < J::PER; ++d) j.o[d] += f * x[d];
+        for (int d = 0; d < J::PER; ++d) j.o[d] += x[d] * h[i] * f;
     }
     j.finish(a, r, (int)g, lane);
 }
@@ -715,14 +752,13 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
     }
     const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
     uint32_t qf[NT][MT][2];
-    float hs[NT][2], acc[NT][MT][4], m_run[NT][2], l_run[NT][2];
-    float v_ref = DQ_VMIN, v_inv = 1.f / DQ_VMIN;
+    float hs[NT][2], acc[NT][MT][4], m_run[NT][2], l_run[NT][2], o_run[NT][2], unit[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            m_run[nt][i] = -INFINITY;
-            l_run[nt][i] = 0.f;
+            m_run[nt][i] = o_run[nt][i] = -INFINITY;
+            l_run[nt][i] = unit[nt][i] = 0.f;
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -739,6 +775,7 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
         }
     }
     uint32_t left = landed ? valid : 0u;
+    Spread spread;
     auto next_tile = [&]() -> Tile {  // the lowest of `left`
         const int s = __ffs(left) - 1;
         left &= left - 1;
@@ -748,12 +785,16 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
 #pragma unroll 1
     while (left) {
         const Tile t0 = next_tile();
-        if (left) {
-            const Tile pair[2] = {t0, next_tile()};
-            attend_codes<D, NT, FMT, 2>(pair, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+        const uint32_t others = left;
+        const Tile two[2] = {t0, left ? next_tile() : t0};
+        bool pair, far;
+        spread.next(t0.vs, two[1].vs, pair, far);
+        if (others && pair) {
+            attend_codes<D, NT, FMT, 2>(two, qf, hs, acc, m_run, l_run, o_run, unit, false, lane);
         } else {
             const Tile one[1] = {t0};
-            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, v_ref, v_inv, lane);
+            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, o_run, unit, far, lane);
+            left = others;  // the second one waits for the next round
         }
     }
     __syncthreads();  // every warp is done with its tiles (after a timeout: with its bounded wait)
@@ -768,15 +809,15 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
             v += __shfl_xor_sync(FULL, v, 16);
             if (g4 == 0) {
                 s_ml[warp][head][0] = m_run[nt][i];
-                s_ml[warp][head][1] = v * DQ_PUNIT;
+                s_ml[warp][head][1] = v;
             }
             if (head < a.G && valid) {  // divided by its sum, as in k_decode_quant
                 float *o = s_o + (warp * a.G + head) * D + 2 * g4;
-                const float inv = v > 0.f ? 1.f / v : 0.f;
+                const float inv = v > 0.f ? __fdividef(DQ_PUNIT, v) : 0.f, half = exp2f(0.5f * (o_run[nt][i] - m_run[nt][i]));
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * v_ref,
-                                                                           acc[nt][mt][2 + i] * inv * v_ref);
+                    *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * half * half,
+                                                                           acc[nt][mt][2 + i] * inv * half * half);
             }
         }
     __syncthreads();
@@ -787,20 +828,21 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
         float2 o = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][head][0]);
-        float f[WARPS];
+        float f[WARPS];  // roots of the weights, as in Joined
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
             const float m = s_ml[w][head][0];
-            f[w] = m == -INFINITY ? 0.f : exp2f(m - M) * s_ml[w][head][1];
-            l += f[w];
+            f[w] = m == -INFINITY ? 0.f : exp2f(0.5f * (m - M));
+            l += f[w] * f[w] * s_ml[w][head][1];
         }
-        const float share = l > 0.f ? 1.f / l : 0.f;
+        const float share = l > 0.f ? __fdividef(1.f, l) : 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
             if (s_ml[w][head][0] == -INFINITY) continue;
             const float2 x = *reinterpret_cast<const float2 *>(s_o + (w * a.G + head) * D + dim);
-            o.x += f[w] * share * x.x;
-            o.y += f[w] * share * x.y;
+            const float g = f[w] * s_ml[w][head][1] * share;
+            o.x += x.x * f[w] * g;
+            o.y += x.y * f[w] * g;
         }
         const size_t at = (size_t)b * a.Hq + (size_t)h * a.G + head;
         *reinterpret_cast<uint32_t *>(a.out + at * D + dim) = pack_bf16x2(o.x, o.y);

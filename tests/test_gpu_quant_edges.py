@@ -95,3 +95,89 @@ def test_values_of_one_sign_at_the_end_of_the_range(fmt, code, exponent, D, P):
             assert bool(torch.isfinite(out).all()) and float(rel.max()) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18, (k, splits)
             assert bool(torch.isfinite(lse).all())
     assert int(c.err.item()) == 0
+
+
+def attend_mixed(c, q, sel, scale):
+    """64-bit attention with, per output element, what check_mixed needs: each token's logit is exact to
+    (D / 16 + 4) 2^-23 of sum |q_d k_d| and 2^-22 of the largest |logit|."""
+    out, lse, tol, ltol = (np.zeros((len(c.L), c.Hq, c.D)), np.full((len(c.L), c.Hq), -np.inf),
+                           np.zeros((len(c.L), c.Hq, c.D)), np.zeros((len(c.L), c.Hq)))
+    kc, vc = ref.values(c.k, c.fmt), ref.values(c.v, c.fmt)
+    for b in range(len(c.L)):
+        for h in range(c.Hkv):
+            pages = [(c.idx[c.ptr[b] + j], min(c.P, int(c.L[b]) - j * c.P)) for j in sel[b, h] if j >= 0]
+            if not pages:
+                continue
+            K = np.concatenate([kc[p, h, :n] * np.float64(c.ks[p, h]) for p, n in pages])
+            C = np.concatenate([vc[p, h, :n] for p, n in pages])
+            s = np.concatenate([np.full(n, np.float64(c.vs[p, h])) for p, n in pages])
+            for g in range(h * c.Hq // c.Hkv, (h + 1) * c.Hq // c.Hkv):
+                x = scale * (K @ q[b, g])
+                w = np.exp(x - x.max())
+                share = w / w.sum()
+                out[b, g], lse[b, g] = (share * s) @ C, x.max() + np.log(w.sum())
+                # the logits' error, weighing only what has weight
+                dx = (c.D / 16 + 4) * 2.0 ** -23 * scale * (np.abs(K) @ np.abs(q[b, g])) + 2.0 ** -22 * np.abs(x).max()
+                lost = 2.0 ** -35 * np.abs(share * s).max()  # an element of P below fp16's normal numbers
+                tol[b, g] = (np.abs(share * s) * (2.0 ** -11 + 2.0 ** -17 + 2 * dx)) @ np.abs(C) + lost * np.abs(C).sum(0)
+                tol[b, g] += (share * dx).sum() * np.abs(out[b, g]) + 2.0 ** -8 * np.abs(out[b, g]) + 2.0 ** -133
+                ltol[b, g] = (share * dx).sum() + 2.0 ** -20 * (1 + abs(lse[b, g]))
+    return out, lse, tol, ltol
+
+
+def check_mixed(out, lse, want):
+    o, l, tol, ltol = want
+    e = np.abs(out.double().cpu().numpy() - o)
+    assert (e <= tol).all(), (e / tol).max()
+    e = np.abs(lse.double().cpu().numpy() - l)
+    assert (e <= ltol).all(), (e / ltol).max()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("Hq,Hkv,D,P", [(4, 2, 64, 16), (12, 1, 128, 16), (8, 1, 128, 64)])
+@pytest.mark.parametrize("lo,hi,slope", [(-42, 0, 2.0), (-42, 0, -2.0), (-110, 100, 1.4), (-110, 100, -1.4), (-110, 100, 0.0),
+                                         (-3, 3, 5.0)])
+def test_value_scales_far_apart_in_one_row(fmt, Hq, Hkv, D, P, lo, hi, slope):
+    """Pages whose value scales differ by up to 2^210, and whose logits make up for it, or not (slope: logit per power of two,
+    in units of -ln 2 / 2): what carries the output is kept, whatever else the row holds."""
+    c = Case(fmt, [P, 7 * P - 5, 61 * P + 3, 30 * P], Hq, Hkv, D, P, seed=23).fill()
+    exps = c.rng.integers(lo, hi + 1, c.vs.shape)
+    exps[c.rng.random(exps.shape) < 0.2] = hi
+    exps[c.rng.random(exps.shape) < 0.4] = lo
+    c.vs[:] = 2.0 ** exps * c.rng.uniform(1.0, 1.9, exps.shape)
+    # keys near a constant direction, so that a page's key scale sets its logits
+    base = 32.0
+    for b, n in enumerate(c.L):
+        for j in range(-(-int(n) // P)):
+            p, m = c.idx[c.ptr[b] + j], min(P, int(n) - j * P)
+            c.k[p, :, :m] = ref.nearest(base + c.rng.integers(-3, 4, (Hkv, m, D)), fmt)
+    q = torch.from_numpy(1 + 0.1 * c.rng.standard_normal((len(c.L), Hq, D))).to(torch.bfloat16)
+    logit = -slope * np.log(2) / 2 * exps + c.rng.standard_normal(exps.shape)
+    c.ks[:] = logit / (base * np.sqrt(D))
+    cache = c.cache()
+    for k in (7, 32, 62):
+        sel = c.select(k)
+        want = attend_mixed(c, q.double().numpy(), sel, 1 / np.sqrt(D))
+        for splits in (0, 1, 5, 100000):
+            out, lse = decode(c, cache, q.to(DEV), dev(sel), num_splits=splits)
+            check_mixed(out, lse, want)
+    assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pages_of_zeros_and_zero_scales_in_a_row(fmt):
+    """A page of zeros has the smallest scale there is, another program's may have scale 0: neither changes its row."""
+    c = Case(fmt, [16, 400, 33], 4, 2, 64, 16, seed=29).fill()
+    for b in range(3):
+        for j in range(0, -(-int(c.L[b]) // 16), 2):
+            c.vs[c.idx[c.ptr[b] + j]] = [2.0 ** -126, 0.0][j % 4 // 2]
+            if j % 4 == 0:
+                c.v[c.idx[c.ptr[b] + j]] = 0
+    c.v[c.idx[c.ptr[2]]], c.vs[c.idx[c.ptr[2]]] = 0, 2.0 ** -126
+    q, cache = c.queries(), c.cache()
+    for k in (3, 25):
+        sel = c.select(k)
+        want = attend_mixed(c, q.double().numpy(), sel, 1 / 8)
+        for splits in (0, 3):
+            check_mixed(*decode(c, cache, q.to(DEV), dev(sel), num_splits=splits), want)
+    assert int(c.err.item()) == 0
