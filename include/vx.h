@@ -327,10 +327,11 @@ vx_status vx_sparse_decode_noalloc(const vx_geometry *geo, const vx_page_table *
  * Scale of a page and head: the smallest power of two s >= 2^-126 for which every token the
  * page holds has |x| <= qmax * s (qmax 127 or 448).  A token written into slot 0 starts a
  * page: its old scale is forgotten.  Later tokens may raise the scale, never lower it; the
- * codes already there are then divided by the factor and rounded once more (exact for e4m3
+ * codes already there are then divided by the factor (in fp32) and rounded once more (exact for e4m3
  * down to its subnormals, at most half a step of the new scale for int8).  A scale found in a
- * partly filled page may be any positive number (another program's): it is kept while it is
- * large enough.
+ * partly filled page may be any positive number (another program's): the page's new scale is the
+ * larger of it and of the power of two that the new tokens need, so one that is no power of two
+ * may give way to the next power of two although the tokens would just have fitted it.
  * code = x / s rounded to nearest, ties to even (s another program's: the fp32 product
  * x * (1 / s) rounded, in an append and a prefill write alike).
  * Powers of two cost an int8 page up to one bit of its range (the mean is half a bit) and

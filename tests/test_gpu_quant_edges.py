@@ -5,7 +5,7 @@ import torch
 
 import quant_ref as ref
 from paged_block_sparse_kv_b200 import vx
-from test_gpu_quant import DEV, FMTS, Case, check_attention, check_cache, decode, dev, new_rows
+from test_gpu_quant import DEV, FMTS, WRITES, Case, check_attention, check_cache, decode, dev, new_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,103 @@ def test_pages_of_zeros_and_zero_scales_in_a_row(fmt):
         for splits in (0, 3):
             check_mixed(*decode(c, cache, q.to(DEV), dev(sel), num_splits=splits), want)
     assert int(c.err.item()) == 0
+
+
+def plain_write(codes, scales, cen, x, c, L, first):
+    """vx_quant_update of keys (cen an array) or values (None) from the header's text, page by page: scales in fp32, a code
+    the fp32 product x * (1 / s) rounded, older codes times s_old / s when the scale grows, centroids in 64 bits."""
+    f32, row = np.float32, 0
+    for b in range(len(L)):
+        t = int(first[b])
+        while t < int(L[b]):
+            page, slot = c.idx[c.ptr[b] + t // c.P], t % c.P
+            n = min(int(L[b]) - t, c.P - slot)
+            for h in range(c.Hkv):
+                new = x[row:row + n, h].astype(f32)
+                s = f32(ref.pow2_scale(np.abs(new).max(), c.fmt))
+                if slot:
+                    old = scales[page, h]
+                    s = max(s, old)
+                    if s > old:
+                        was = ref.values(codes[page, h, :slot], c.fmt).astype(f32)
+                        codes[page, h, :slot] = ref.nearest((was * (old / s)).astype(np.float64), c.fmt)
+                scales[page, h] = s
+                codes[page, h, slot:slot + n] = ref.nearest((new * (f32(1) / s)).astype(np.float64), c.fmt)
+                if cen is not None:
+                    total = ref.values(codes[page, h, :slot + n], c.fmt).sum(0)
+                    cen[page, h] = ref.to_bf16(np.float64(s) * total / (slot + n))
+            row, t = row + n, t + n
+
+
+def odd_scales(c):
+    """Another program's scales: any fp32 numbers, some of them just under a power of two, some far from ordinary."""
+    for s in (c.ks, c.vs):
+        wild = c.rng.random(s.shape)
+        s[:] = np.where(wild < 0.2, s * f32_pow2(c.rng, s.shape, -90, -80), s)
+        s[:] = np.where((wild > 0.2) & (wild < 0.4), np.nextafter(2.0 ** np.rint(np.log2(s)), 0, dtype=np.float32), s)
+
+
+def f32_pow2(rng, shape, lo, hi):
+    return (2.0 ** rng.integers(lo, hi, shape)).astype(np.float32)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("case", range(len(WRITES)))
+@pytest.mark.parametrize("scales", ["powers", "odd"])
+def test_prefill_into_filled_pages_is_exact(fmt, case, scales):
+    """Scales, all codes (new ones, older ones under a raised scale, untouched slots and pages) and centroids, bit for bit."""
+    L, first, Hkv, D, P = WRITES[case]
+    c = Case(fmt, L, Hkv, Hkv, D, P, seed=100 + case).fill()
+    if scales == "odd":
+        odd_scales(c)
+    else:
+        for s in (c.ks, c.vs):
+            s[:] = 2.0 ** np.rint(np.log2(s))
+    n = int((np.array(L) - np.array(first)).sum())
+    kn, vn = new_rows(c, n), new_rows(c, n)
+    cache = c.cache()
+    cen = torch.full((c.pool, Hkv, D), 0.5, dtype=torch.bfloat16, device=DEV)
+    want = np.full((c.pool, Hkv, D), 0.5)
+    vx.vx_quant_update(c.geo, c.table, cache, cen, kn.to(DEV), vn.to(DEV), first_pos=dev(np.array(first)), err=c.err)
+    plain_write(c.k, c.ks, want, kn.float().numpy(), c, L, first)
+    plain_write(c.v, c.vs, None, vn.float().numpy(), c, L, first)
+    check_cache(c, cache, cen, want)
+    assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("P,D,Hkv", [(16, 128, 8), (32, 64, 1), (64, 128, 2), (64, 64, 4), (16, 64, 16)])
+def test_appends_under_odd_scales_are_exact(fmt, P, D, Hkv):
+    """Tokens appended one by one to pages that another program filled in part, until they are full and others begin."""
+    B, steps = 5, P // 2 + 3
+    c = Case(fmt, [P // 2 + steps + 3 * b for b in range(B)], Hkv, Hkv, D, P, seed=P + D + Hkv).fill()
+    odd_scales(c)
+    cache = c.cache()
+    cen = torch.full((c.pool, Hkv, D), 0.5, dtype=torch.bfloat16, device=DEV)
+    want = np.full((c.pool, Hkv, D), 0.5)
+    for step in range(steps):
+        lens = c.L - steps + step + 1
+        kn, vn = new_rows(c, B, 6), new_rows(c, B, 6)
+        t = vx.PageTable(c.table.page_ptr, c.table.page_indices, dev(lens), c.max_pages)
+        vx.vx_quant_update(c.geo, t, cache, cen, kn.to(DEV), vn.to(DEV), err=c.err)
+        plain_write(c.k, c.ks, want, kn.float().numpy(), c, lens, lens - 1)
+        plain_write(c.v, c.vs, None, vn.float().numpy(), c, lens, lens - 1)
+        check_cache(c, cache, cen, want)
+    assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+def test_an_odd_scale_gives_way_to_the_power_of_two_the_token_needs(prefill):
+    """0.9 * 127 = 114 would hold a token of 100, whose power of two is 1: the scale becomes 1, the older codes times 0.9."""
+    c = Case("int8", [4], 1, 1, 64, 16, seed=1).fill()
+    page = c.idx[0]
+    c.ks[page] = c.vs[page] = 0.9
+    c.k[page, 0, :3] = c.v[page, 0, :3] = np.arange(-96, 96, dtype=np.int64).reshape(3, 64).astype(np.int8).view(np.uint8)
+    cache, cen = c.cache(), torch.zeros(c.pool, 1, 64, dtype=torch.bfloat16, device=DEV)
+    x = torch.full((1, 1, 64), 100.0, dtype=torch.bfloat16, device=DEV)
+    vx.vx_quant_update(c.geo, c.table, cache, cen, x, x, first_pos=dev([3]) if prefill else None, err=c.err)
+    assert float(cache.k_scale[page]) == 1 and float(cache.v_scale[page]) == 1
+    was = np.arange(-96, 96).astype(np.float32) * np.float32(0.9)  # in fp32, where 95 * 0.9 is the tie 85.5
+    for a in (cache.k_cache, cache.v_cache):
+        got = a[page, 0].cpu().numpy()
+        assert np.array_equal(got[:3].ravel(), np.rint(was)) and (got[3] == 100).all()
