@@ -468,11 +468,14 @@ __global__ void __launch_bounds__(PG_BLOCK) k_apply_update(const PageArgs a, con
             copy_piece(a, plan.tail, free_pages.page_of((uint32_t)plan.off, lane), job - item * jobs.pieces);
     } else if (is_row) {  // entries taken over from the parent
         int32_t id[PG_SPAN / 32];
+        bool bad_id = false;
 #pragma unroll
         for (int u = 0; u < PG_SPAN / 32; ++u) {
             const int j = j0 + 32 * u + lane;
-            if (j < plan.held) id[u] = a.page_indices[plan.from + j];
+            id[u] = j < plan.held ? a.page_indices[plan.from + j] : 0;
+            bad_id |= id[u] < 0 || id[u] >= a.num_pages;
         }
+        if (bad_id) set_err(a.err, VX_DATA_BAD_PAGE_ID);
 #pragma unroll
         for (int u = 0; u < PG_SPAN / 32; ++u) {
             const int j = j0 + 32 * u + lane;
