@@ -50,7 +50,7 @@ vx_status check_geometry(const vx_geometry *g) {
     if (g->num_pool_pages < 1) return fail(VX_ERR_INVALID_ARG, "num_pool_pages must be >= 1");
     if (g->page_size < 1 || g->head_dim_qk < 1 || g->head_dim_v < 1)
         return fail(VX_ERR_INVALID_ARG, "page_size and head dims must be >= 1");
-    if (g->num_pool_pages * (int64_t)g->num_kv_heads > INT32_MAX)
+    if (g->num_pool_pages > INT32_MAX / g->num_kv_heads)
         return fail(VX_ERR_INVALID_ARG, "num_pool_pages * num_kv_heads overflows int32");
     const int G = g->num_q_heads / g->num_kv_heads;
     if (g->page_size != 16 && g->page_size != 32 && g->page_size != 64)

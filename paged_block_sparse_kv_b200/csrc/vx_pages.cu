@@ -31,7 +31,7 @@ vx_status check_word_ptr(const void *p, const char *name, bool can_be_null = fal
 vx_status check_pool(const vx_geometry *g, const vx_page_pool *p) {
     if (!p) return bad(VX_ERR_INVALID_ARG, "page pool is NULL");
     if (p->elem_bytes != 1 && p->elem_bytes != 2) return bad(VX_ERR_INVALID_ARG, "elem_bytes must be 1 or 2");
-    if (p->num_pages < 1 || p->num_pages * (int64_t)g->num_kv_heads > INT32_MAX)
+    if (p->num_pages < 1 || p->num_pages > INT32_MAX / g->num_kv_heads)
         return bad(VX_ERR_INVALID_ARG, "num_pages must be >= 1, and num_pages * num_kv_heads fit int32");
     VX_TRY(vx::validate_ptr(p->k_cache, "pool k_cache", false));
     if (!g->mla_shared_kv) VX_TRY(vx::validate_ptr(p->v_cache, "pool v_cache", false));

@@ -49,3 +49,12 @@ def test_compaction_counts_apart_and_misaligned(L, off, pages):
 def test_more_new_rows_than_31_bits(L):
     c = ctypes.byref(vx.vx_quant_cache(vx.VX_QUANT_INT8, FAKE, FAKE, FAKE, FAKE))
     assert L.vx_quant_update(_geo(), _table(), c, FAKE, FAKE, FAKE, 1 << 31, FAKE, None, None) == vx.VX_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("pages", [1 << 31, 1 << 60, 1 << 61, (1 << 63) - 1])
+def test_pools_of_more_pages_than_31_bits_times_heads(L, pages):
+    """Also where the product of pages and heads wraps in 64 bits to a small number."""
+    n = L.vx_page_workspace_size(_geo(), 1)
+    assert L.vx_copy_pages(_geo(), _pool(num_pages=pages), _pool(k_cache=FAR, v_cache=FAR + (1 << 33)), FAKE, FAKE, 1, FAKE,
+                           n, None, None) == INVALID
+    assert L.vx_page_workspace_size(_geo(num_pool_pages=pages), 1) == 0
