@@ -473,7 +473,7 @@ vx_status vx_compact_pages(const vx_geometry *geo, const vx_page_pool *pool, con
                            int32_t *num_live, void *ws, size_t ws_bytes, int32_t *err, void *stream);
 
 /* Workspace bytes of the three page calls for pools of geo->num_pool_pages pages and at most
- * `rows` new rows; 0 when the arguments are invalid (see vx_last_error). */
+ * `rows` new rows, whatever geo->batch is; 0 when the arguments are invalid (see vx_last_error). */
 size_t vx_page_workspace_size(const vx_geometry *geo, int32_t rows);
 
 /*

@@ -75,7 +75,9 @@ void table_args(vx::PageArgs *a, const vx_geometry *g, const vx_page_table *t) {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: head words, a word per page (the copy's claims) or per 32 pages (flags, whole segments
-// of 1024 pages), a count per segment, four words per new row, one per old row, two per possible move.
+// of 1024 pages), a count per segment, four words per new row, one per old row (of the largest batch:
+// the size depends on the pool and the new rows alone, and a workspace serves as the batch changes),
+// two per possible move.
 struct PageWs {
     size_t a, b, c, d, e, f, total;
 };
@@ -86,7 +88,7 @@ PageWs page_ws(const vx_geometry *g, int32_t rows) {
     w.b = w.a + up256(std::max(n, segs * 32) * sizeof(int32_t));
     w.c = w.b + up256(segs * sizeof(int32_t));
     w.d = w.c + up256((size_t)rows * 4 * sizeof(int32_t));
-    w.e = w.d + up256((size_t)g->batch * sizeof(int32_t));
+    w.e = w.d + up256((size_t)MAX_ROWS * sizeof(int32_t));
     w.f = w.e + up256((n / 2 + 1) * sizeof(int32_t));
     w.total = w.f + up256((n / 2 + 1) * sizeof(int32_t));
     return w;

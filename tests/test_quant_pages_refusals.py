@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from paged_block_sparse_kv_b200 import vx
 
@@ -58,3 +59,16 @@ def test_pools_of_more_pages_than_31_bits_times_heads(L, pages):
     assert L.vx_copy_pages(_geo(), _pool(num_pages=pages), _pool(k_cache=FAR, v_cache=FAR + (1 << 33)), FAKE, FAKE, 1, FAKE,
                            n, None, None) == INVALID
     assert L.vx_page_workspace_size(_geo(num_pool_pages=pages), 1) == 0
+
+
+def test_page_workspace_serves_every_batch(L):
+    """A workspace for a pool and its new rows is large enough whatever the number of old rows of the call is."""
+    n = L.vx_page_workspace_size(_geo(batch=1), 7)
+    for batch in (1, 2, 500, 4096):
+        g = _geo(batch=batch)
+        assert L.vx_page_workspace_size(g, 7) == n
+        call = lambda size: L.vx_update_table(g, _pool(), _table(), FAKE, FAKE, FAKE, 7, FAKE, FAR, 100, FAR + 4096, 4, FAKE,
+                                              FAKE, size, None, None)
+        # (without a GPU the launch fails, after every check of the arguments)
+        assert call(n) not in (vx.VX_ERR_WORKSPACE, INVALID) if not torch.cuda.is_available() else True
+        assert call(n - 1) == vx.VX_ERR_WORKSPACE
