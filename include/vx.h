@@ -413,7 +413,8 @@ typedef struct {
 /*
  * Copy pages: for i < num_copies, page src_pages[i] of `src` to page dst_pages[i] of `dst`
  * (device int32 arrays), all arrays of the pools.  Both pools have geo's page layout and the
- * same arrays; `src` and `dst` may be one pool (the same k_cache).  dst->num_pages must be
+ * same arrays; `src` and `dst` may be one pool (the same k_cache and all else), or share no
+ * memory (VX_ERR_INVALID_ARG).  dst->num_pages must be
  * geo->num_pool_pages.  geo->batch is not used (but valid).
  * A copy whose destination an earlier copy of the call names, or (in one pool) any copy names
  * as a source, sets VX_DATA_BAD_COPY and is not made; one with a page outside its pool sets

@@ -133,6 +133,20 @@ bool overlap(const void *a, size_t an, const void *b, size_t bn) {
     return x < y + bn && y < x + an;
 }
 
+// Any array of one pool shares memory with any array of the other
+bool pools_overlap(const vx_page_pool *p, const vx_page_pool *q, const vx::PageArgs &a) {
+    const size_t bytes[5] = {(size_t)a.kb, (size_t)a.vb, (size_t)a.cb, p->k_scale ? (size_t)a.Hkv * 4 : 0,
+                             p->k_scale ? (size_t)a.Hkv * 4 : 0};  // of a page, in both pools
+    const void *x[5] = {p->k_cache, p->v_cache, p->centroids, p->k_scale, p->v_scale};
+    const void *y[5] = {q->k_cache, q->v_cache, q->centroids, q->k_scale, q->v_scale};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < 5; ++j)
+            if (bytes[i] && bytes[j] &&
+                overlap(x[i], (size_t)p->num_pages * bytes[i], y[j], (size_t)q->num_pages * bytes[j]))
+                return true;
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -163,12 +177,7 @@ vx_status vx_copy_pages(const vx_geometry *geo, const vx_page_pool *src, const v
     if (one && (src->v_cache != dst->v_cache || src->centroids != dst->centroids || src->k_scale != dst->k_scale ||
                 src->v_scale != dst->v_scale || src->num_pages != dst->num_pages))
         return bad(VX_ERR_INVALID_ARG, "pools that share k_cache must be the same pool");
-    if (!one && (overlap(src->k_cache, (size_t)src->num_pages * a.kb, dst->k_cache, (size_t)dst->num_pages * a.kb) ||
-                 (a.vb && overlap(src->v_cache, (size_t)src->num_pages * a.vb, dst->v_cache,
-                                  (size_t)dst->num_pages * a.vb)) ||
-                 (a.cb && overlap(src->centroids, (size_t)src->num_pages * a.cb, dst->centroids,
-                                  (size_t)dst->num_pages * a.cb))))
-        return bad(VX_ERR_INVALID_ARG, "two pools must not overlap in memory");
+    if (!one && pools_overlap(src, dst, a)) return bad(VX_ERR_INVALID_ARG, "two pools must not overlap in memory");
     if (num_copies == 0) return VX_OK;
     VX_TRY(check_word_ptr(src_pages, "src_pages"));
     VX_TRY(check_word_ptr(dst_pages, "dst_pages"));

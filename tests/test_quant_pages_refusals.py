@@ -72,3 +72,22 @@ def test_page_workspace_serves_every_batch(L):
         # (without a GPU the launch fails, after every check of the arguments)
         assert call(n) not in (vx.VX_ERR_WORKSPACE, INVALID) if not torch.cuda.is_available() else True
         assert call(n - 1) == vx.VX_ERR_WORKSPACE
+
+
+def test_copies_between_pools_that_share_any_array(L):
+    """Scales, centroids, and one pool's keys under the other's values: a copy would overwrite what another copy reads."""
+    n = L.vx_page_workspace_size(_geo(), 1)
+
+    def copy(**kw):
+        src = dict(elem_bytes=1, centroids=1 << 36, k_scale=1 << 37, v_scale=(1 << 37) + (1 << 30))
+        dst = dict(elem_bytes=1, k_cache=FAR, v_cache=FAR + (1 << 34), centroids=FAR + (1 << 36), k_scale=FAR + (1 << 37),
+                   v_scale=FAR + (1 << 37) + (1 << 30))
+        dst.update(kw)
+        return L.vx_copy_pages(_geo(), _pool(**src), _pool(**dst), FAKE, FAKE, 0, FAKE, n, None, None)
+
+    assert copy() == vx.VX_OK  # no copies: nothing is launched
+    last = 5000 * 8 * 4 - 4  # the last scale
+    for kw in (dict(k_scale=1 << 37), dict(v_scale=(1 << 37) + last), dict(k_scale=(1 << 37) + (1 << 30) - last),
+               dict(centroids=(1 << 36) + 4096), dict(v_cache=1 << 30), dict(k_cache=(1 << 34) + 16)):
+        assert copy(**kw) == INVALID, kw
+    assert copy(k_scale=(1 << 37) + last + 4) == vx.VX_OK
