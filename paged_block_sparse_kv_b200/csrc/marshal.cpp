@@ -185,6 +185,9 @@ struct Table : vx_page_table {
     }
 };
 
+// [a, a + an) and [b, b + bn) int32 entries have one in common
+bool overlap(const int32_t *a, int64_t an, const int32_t *b, int64_t bn) { return a < b + bn && b < a + an; }
+
 ScalarType type_of(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) throw TypeErr(std::string(name) + " must be a tensor");
     return THPVariable_Unpack(o).scalar_type();
@@ -340,6 +343,12 @@ PyObject *update_table(PyObject *const *a) {
     size_t n;
     void *ws = c.workspace(a[8], &n);
     int32_t *err = c.err(a[9]);
+    if (overlap(to.page_indices, to.entries, t.page_indices, t.entries) ||
+        overlap(to.page_indices, to.entries, t.seq_lens, g.batch) || overlap(to.page_indices, to.entries, t.page_ptr, g.batch))
+        throw ValueErr("the new table's page_indices must not lie in the old table's memory");
+    if (overlap(to.seq_lens, rows, t.page_indices, t.entries) || overlap(to.seq_lens, rows, t.seq_lens, g.batch) ||
+        overlap(to.seq_lens, rows, t.page_ptr, g.batch))
+        throw ValueErr("the new table's seq_lens must not lie in the old table's memory");
     return c.run(a[10], [&](void *s) {
         return fn.update_table(&g, &pool, &t, ref, parent, grow, (int32_t)rows, to.page_ptr,
                                const_cast<int32_t *>(to.page_indices), to.entries, const_cast<int32_t *>(to.seq_lens),
@@ -358,6 +367,8 @@ PyObject *compact_pages(PyObject *const *a) {
     int32_t *idx = c.flat<int32_t>(a[4], "new_indices", ScalarType::Int);
     if (idx && THPVariable_Unpack(a[4]).numel() != t.entries)
         throw ValueErr("new_indices must have as many entries as the table's page_indices");
+    if (idx && idx != t.page_indices && overlap(idx, t.entries, t.page_indices, t.entries))
+        throw ValueErr("new_indices must be the table's page_indices or apart from them");
     int32_t *new_ref = c.ptr<int32_t>(a[5], "new_ref", ScalarType::Int, {N});
     int32_t *remap = c.ptr<int32_t>(a[6], "remap", ScalarType::Int, {N});
     int32_t *live = c.ptr<int32_t>(a[7], "num_live", ScalarType::Int, {1});

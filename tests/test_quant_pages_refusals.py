@@ -91,3 +91,29 @@ def test_copies_between_pools_that_share_any_array(L):
                dict(centroids=(1 << 36) + 4096), dict(v_cache=1 << 30), dict(k_cache=(1 << 34) + 16)):
         assert copy(**kw) == INVALID, kw
     assert copy(k_scale=(1 << 37) + last + 4) == vx.VX_OK
+
+
+def test_binding_refuses_new_tables_in_the_old_ones_memory():
+    """The C call knows the old page_indices' start alone; the binding knows its extent."""
+    geo = vx.Geometry(2, 4, 2, 64, 64, 16, False, 10)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    codes = torch.zeros(10, 2, 16, 64, dtype=torch.int8)
+    pool, both = vx.PagePool(codes, codes.clone()), i32(40)
+    old = vx.PageTable(i32(2), both[:24], i32(2), 4)
+    call = lambda idx, lens=None: vx.vx_update_table(geo, pool, old, i32(10), i32(2), i32(2),
+                                                     vx.PageTable(i32(2), idx, i32(2) if lens is None else lens, 4), i32(10),
+                                                     i32(8))
+    for idx in (both[16:32], both[23:], both[:24], both[4:8], old.seq_lens):
+        with pytest.raises(ValueError, match="old table's memory"):
+            call(idx)
+    for lens in (both[22:24], old.seq_lens, old.page_ptr):
+        with pytest.raises(ValueError, match="old table's memory"):
+            call(i32(16), lens)
+    with pytest.raises(ValueError, match="CUDA"):  # apart: the next check
+        call(both[24:])
+    compact = lambda idx: vx.vx_compact_pages(geo, pool, old, i32(10), idx, i32(10), i32(10), i32(1), i32(8))
+    with pytest.raises(ValueError, match="apart"):
+        compact(both[8:32])
+    for idx in (both[:24], i32(24)):
+        with pytest.raises(ValueError, match="CUDA"):
+            compact(idx)
