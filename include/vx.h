@@ -322,7 +322,8 @@ vx_status vx_sparse_decode_noalloc(const vx_geometry *geo, const vx_page_table *
  *   first_pos == NULL: append one token per request (k_new, v_new [B][Hkv][D], bf16).
  *   first_pos != NULL: prefill write, k_new and v_new [N][Hkv][D] packed in request order.
  * Positions, tables and errors are those of vx_centroid_update.
- *   num_new: rows of k_new and v_new (append: at least B; below 2^31).  A prefill request whose rows would
+ *   num_new: rows of k_new and v_new (append: at least B; below 2^31; a prefill write of 0 rows
+ *   writes nothing and may have NULL there).  A prefill request whose rows would
  *   pass it sets VX_DATA_BAD_SEQ_LEN and writes nothing.
  * Scale of a page and head: the smallest power of two s >= 2^-126 for which every token the
  * page holds has |x| <= qmax * s (qmax 127 or 448).  A token written into slot 0 starts a

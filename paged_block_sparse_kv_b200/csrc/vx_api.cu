@@ -828,8 +828,9 @@ vx_status vx_quant_update(const vx_geometry *geo, const vx_page_table *table, co
     VX_TRY(check_geo(geo, table));
     VX_TRY(check_quant(geo, cache));
     VX_TRY(check_ptr(centroids, "centroids"));
-    VX_TRY(check_ptr(k_new, "k_new"));
-    VX_TRY(check_ptr(v_new, "v_new"));
+    const bool none = first_pos && num_new == 0;  // no rows, no arrays (an empty tensor's pointer is NULL)
+    VX_TRY(check_ptr(k_new, "k_new", none));
+    VX_TRY(check_ptr(v_new, "v_new", none));
     if (first_pos && !al4(first_pos)) return fail(VX_ERR_INVALID_ARG, "first_pos must be 4-byte aligned");
     if (err && !al4(err)) return fail(VX_ERR_INVALID_ARG, "err must be 4-byte aligned");
     if (num_new < 0 || (!first_pos && num_new < geo->batch))

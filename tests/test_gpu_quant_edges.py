@@ -281,3 +281,16 @@ def test_an_odd_scale_gives_way_to_the_power_of_two_the_token_needs(prefill):
     for a in (cache.k_cache, cache.v_cache):
         got = a[page, 0].cpu().numpy()
         assert np.array_equal(got[:3].ravel(), np.rint(was)) and (got[3] == 100).all()
+
+
+@pytest.mark.parametrize("P", [16, 64])
+def test_prefill_of_no_rows(P):
+    """A step in which no request brings tokens: an empty tensor's pointer is NULL, and nothing is written."""
+    c = Case("e4m3", [P, 3 * P + 1, 5], 2, 2, 64, P, seed=7).fill()
+    cache, cen = c.cache(), torch.full((c.pool, 2, 64), 0.5, dtype=torch.bfloat16, device=DEV)
+    x = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    vx.vx_quant_update(c.geo, c.table, cache, cen, x, x, first_pos=dev(c.L), err=c.err)
+    assert int(c.err.item()) == 0
+    vx.vx_quant_update(c.geo, c.table, cache, cen, x, x, first_pos=dev(c.L - 1), err=c.err)
+    assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN  # rows that are not there
+    check_cache(c, cache, cen, np.full((c.pool, 2, 64), 0.5))
