@@ -303,8 +303,9 @@ __device__ __forceinline__ void load_query(const __nv_bfloat16 *qb, int G, float
         uint32_t amax = max(top & 0xffffu, top >> 16);
         amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
         amax = max(amax, __shfl_xor_sync(FULL, amax, 2));
-        // 2^(14 - exponent of the largest element), kept in fp32's normal range
-        const uint32_t ef = min(268u - (amax >> 7), 253u);
+        // 2^(14 - exponent of the largest element), at most 2^113: that takes bf16's smallest number to 2^-20,
+        // still exact in fp16, and leaves its inverse 13 bits above fp32's smallest normal number for sm_scale
+        const uint32_t ef = min(268u - (amax >> 7), 240u);
         const float mul = __uint_as_float(ef << 23);
         const float inv = __uint_as_float((254u - ef) << 23) * scale_log2;
 #pragma unroll

@@ -294,3 +294,22 @@ def test_prefill_of_no_rows(P):
     vx.vx_quant_update(c.geo, c.table, cache, cen, x, x, first_pos=dev(c.L - 1), err=c.err)
     assert int(c.err.item()) == vx.VX_DATA_BAD_SEQ_LEN  # rows that are not there
     check_cache(c, cache, cen, np.full((c.pool, 2, 64), 0.5))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tiny_queries_under_large_key_scales(fmt):
+    """Queries among bf16's smallest numbers, keys whose scales make up for it, and a small sm_scale: their product is
+    ordinary, and so is its precision."""
+    c = Case(fmt, [90, 200, 700], 4, 2, 64, 16, seed=31).fill()
+    q = (c.queries().double() * torch.tensor([2.0 ** -126, 2.0 ** -112, 2.0 ** -99])[:, None, None]).to(torch.bfloat16)
+    for b, e in enumerate((126, 118, 104)):
+        pages = c.idx[c.ptr[b]:c.ptr[b] + -(-int(c.L[b]) // 16)]
+        c.ks[pages] = 2.0 ** (e - c.rng.integers(0, 3, c.ks[pages].shape)) * c.rng.uniform(0.6, 0.9, c.ks[pages].shape)
+    sel, cache = c.select(44), c.cache()
+    for sm in (2.0 ** -9, 2.0 ** -14):
+        want = attend_mixed(c, q.double().numpy(), sel, sm)
+        for splits in (0, 4):
+            check_mixed(*decode(c, cache, q.to(DEV), dev(sel), num_splits=splits, sm_scale=sm), want)
+    sel = sel[:, :, :5]
+    check_mixed(*decode(c, cache, q.to(DEV), dev(sel), sm_scale=2.0 ** -12), attend_mixed(c, q.double().numpy(), sel, 2.0 ** -12))
+    assert int(c.err.item()) == 0
