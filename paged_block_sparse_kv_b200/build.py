@@ -38,10 +38,24 @@ def _stale():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def marshal_mark() -> str:
+    """What _vx_marshal.so was built for: its docstring.  Its layout of tensors is that of one torch, one Python."""
+    import torch
+    return f"vx marshal for torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _marshal_stale():
+    if not os.path.exists(MARSHAL):
+        return True
+    t = os.path.getmtime(MARSHAL)
+    if any(os.path.getmtime(p) > t for p in (MARSHAL_SRC, os.path.join(ROOT, "include", "vx.h"))):
+        return True
+    with open(MARSHAL, "rb") as f:
+        return marshal_mark().encode() + b"\0" not in f.read()
+
+
 def build_marshal(force: bool = False) -> str:
-    header = os.path.join(ROOT, "include", "vx.h")
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(MARSHAL) >= os.path.getmtime(p)
-                                                     for p in (MARSHAL_SRC, header)):
+    if not force and not _marshal_stale():
         return MARSHAL
     import sysconfig
 
@@ -51,6 +65,7 @@ def build_marshal(force: bool = False) -> str:
     tmp = MARSHAL + ".tmp"
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, MARSHAL_SRC,
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    f'-DVX_MARSHAL_MARK="{marshal_mark()}"',
                     "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
                     "-isystem", os.path.join(cuda, "include"), "-L" + os.path.join(base, "lib"),
                     "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)

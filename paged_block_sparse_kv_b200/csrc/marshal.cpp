@@ -424,7 +424,8 @@ PyMethodDef methods[] = {
     METHOD("update_table", update_table, 11),
     METHOD("compact_pages", compact_pages, 11),
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_vx_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// the docstring says what the module was built for (see build.py)
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_vx_marshal", VX_MARSHAL_MARK, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

@@ -281,11 +281,14 @@ _native = None
 
 
 def _marshal():
-    """The loaded _vx_marshal, bound to libvx.so's entry points (raises if it has not been built)."""
+    """The loaded _vx_marshal, bound to libvx.so's entry points (raises if it has not been built, or for another torch)."""
     global _native
     if _native is None:
         L = lib()
         from . import _vx_marshal as m
+        from .build import marshal_mark
+        if m.__doc__ != marshal_mark():
+            raise ImportError(f"_vx_marshal.so is a {m.__doc__}, this is {torch.__version__}; run __graft_entry__.build()")
         m.bind(*[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in
                  ("vx_quant_update", "vx_sparse_decode_quant", "vx_block_topk_decode_quant",
                   "vx_block_topk_decode_append_quant", "vx_copy_pages", "vx_update_table", "vx_compact_pages")])
