@@ -28,12 +28,15 @@
 // Value codes past the request's length are zeroed in registers, logits there are -inf.
 //
 // Bound: HBM (2 bytes read per token, KV head and dim for 4 G operations).  Measured on one B200,
-// whole call: 256 requests of 64 pages (543 MB) 104 us, 5.2 TB/s, the decode kernel alone 5.9 TB/s;
-// 32 requests of 128 pages (135 MB) 32.9 us, 4.1 TB/s: 3 us until the first copies leave (selection,
+// whole call: 256 requests of 64 pages (543 MB) 105 us, 5.2 TB/s, the decode kernel alone 5.5 TB/s;
+// 32 requests of 128 pages (135 MB) 33.5 us, 4.0 TB/s: 3 us until the first copies leave (selection,
 // then page table, both from DRAM), warps that end over 9 us (22 to 31 us), the merge.  The
-// conversions are hidden: with none at all (a timing copy) 256 requests take 0.5% and 32 requests 0.3%
-// less.  16 warps per SM because a tile is a chain of short steps: 8 warps took 137 us where 16 take
-// 108; the ring then holds 3 tiles per warp, the same 192 KB.
+// conversions are hidden: with none at all (a timing copy) 256 requests took 0.5% and 32 requests 0.3%
+// less.  16 warps per SM because a tile is a chain of short steps: 8 warps took 137 us where 16 took
+// 108; the ring then holds 3 tiles per warp, the same 192 KB.  Units that follow the weights (see
+// attend_codes) and partials divided by their sums cost 256 requests 1.5% and 32 requests 1.3%; an
+// integer exponent as the unit took 107.5 us where this takes 106.3, weights computed ahead of the
+// maximum 108.2.
 // Measured and not kept: the block joining its warps' partials itself (its loads of fresh partials
 // cost 4-5 us at the block's end: 37.5 and 33.0 us), the first two tiles issued before the rest (33.3
 // and 32.7), the selection's lines prefetched before the dependency wait (34.9 and 32.7).
@@ -49,8 +52,8 @@ namespace vx {
 namespace {
 
 // Partials per row above which the merge takes a block per row and head (k_merge_many).  Against
-// k_merge, us per call: 85 partials per row 20.0 and 20.7, 296 15.6 and 18.5, 1,024 23.4 and 33.7; but
-// 18 per row 23.0 and 21.9.
+// k_merge, us per call: 61 partials per row 18.3 and 19.8, 128 12.2 and 15.5, 256 13.1 and 19.3, 512 21.3
+// and 32.2; but 16 per row 22.4 and 21.8, 32 9.0 and 8.6.
 constexpr int DQ_MANY = 32;
 constexpr int DQ_FEW = 4;            // at most this many: k_merge_few
 constexpr float DQ_PSHIFT = 15.f;       // weights are at most 2^15, fp16's largest number is 65504

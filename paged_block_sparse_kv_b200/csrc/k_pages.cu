@@ -9,10 +9,10 @@
 // job: these kernels run a few microseconds, and instructions are fetched cold.
 // Page data moves in pieces of PG_PIECE 16-byte chunks.  Bound: HBM for page data (read and
 // written once), a few dependent loads for the rest.
-// Measured on one B200: 8,192 pages of 67.6 KB from pool to pool 178 us (6.2 TB/s, 0.95 of the copy
-// peak), a half empty pool of 32,768 such pages compacted in 187 us (5.9 TB/s); 5 pages 3.6 us; new
-// rows of 256 requests over 290,000 pages 9.1 us, of 64 beams 7.2 us; 500 latent pages compacted in
-// 6.8 us.  Measured and not kept: bulk copies through shared memory (185-189 us in 2-4 blocks of 3 x 16 KB
+// Measured on one B200: 8,192 pages of 67.6 KB from pool to pool 179 us (6.2 TB/s, 0.95 of the copy
+// peak), a half empty pool of 32,768 such pages compacted in 188 us (5.9 TB/s); 5 pages 3.7 us; new
+// rows of 256 requests over 290,000 pages 9.2 us, of 64 beams 7.4 us; 500 latent pages compacted in
+// 6.9 us.  Measured and not kept: bulk copies through shared memory (185-189 us in 2-4 blocks of 3 x 16 KB
 // per SM, where plain loads took 183), one flat list of all chunks (187), pieces of 1,280 to 2,304
 // chunks (179-190 us).
 #include <cooperative_groups.h>

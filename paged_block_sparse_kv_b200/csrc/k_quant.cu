@@ -19,12 +19,13 @@
 //    16-byte chunks.  Value codes are read only when the scale grows.  Latency bound (length ->
 //    table -> codes).
 // Measured on one B200: prefill of 8 ragged requests, 16-token pages, head_dim 128, e4m3 (833 MB): 144 us
-// warm and alone (0.88 of the copy peak), 150 in turn with other work (0.85).  Shortest of four graph
+// warm and alone (0.88 of the copy peak), 151 in turn with other work (0.84).  Shortest of four graph
 // replays, which flatters: e4m3 139 us, int8 144, 64-token pages 154; head_dim 64 0.58-0.66 of the copy
 // peak (a unit is half as long and its fixed part the same).  Four blocks per SM (64 registers): three
 // took 156 us where four took 147 and two 174.  A grid of requests by pages, whose blocks past a short
 // request's end do nothing, took 151 us where this list takes 144 (and 486 where this one takes 507 for
-// 256 of equal length).  Append of 256 requests, 8 KV heads 5.6 us.
+// 256 of equal length).  Append of 256 requests, 8 KV heads 5.7 us.  The bound of four blocks costs
+// spills at head_dim 128: 44-48 bytes in k_quant_prefill, 364-380 in quant_unit (a chunk's first page).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

@@ -157,7 +157,7 @@ vx_status plan(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p, int
         if (quant) {
             // an even number of tiles per chunk (they are attended in pairs), at least 4, or 2 when 4
             // would leave most SMs without a chunk.  Chunks and us against one chunk per warp: 16,384
-            // tiles in chunks of 8 21.2 and 22.3, 10,192 of 6 18.5 and 20.3, 4,096 of 4 10.8 and 12.4
+            // tiles in chunks of 8 21.8 and 22.3, 10,192 of 6 18.2 and 19.9, 4,096 of 4 12.2 and 15.2
             int64_t per = std::max<int64_t>((p->units + w - 1) / w, p->units >= 4 * sms ? 4 : 2);
             per += per & 1;
             w = (p->units + per - 1) / per;
@@ -278,9 +278,9 @@ size_t decode_ws_bytes(const WsLayout &l) { return l.scores; }
 // The 8-bit decode's plan: plan() for its own count of warps and with its own rule for chunks.
 // Planned, short rows, and no more of them than fit the GPU at once: a block per row, whose warps join
 // their partials in shared memory, instead of a split over the GPU and a merge kernel.  Measured,
-// split and row (us): 32 rows of 8 tiles 7.9 and 4.4, 128 of 32 10.8 and 8.1, 256 of 16 10.3 and 7.3,
-// 512 of 8 10.3 and 7.7; a second wave costs more: 256 of 32 14.5 and 16.3, 512 of 16 15.5 and 15.8,
-// 2,048 of 8 24.6 and 28.4.
+// split and row (us): 32 rows of 8 tiles 7.9 and 4.6, 128 of 32 11.1 and 8.6, 256 of 16 10.8 and 8.3,
+// 512 of 8 10.6 and 8.0; a second wave costs more: 256 of 32 14.5 and 18.3, 512 of 16 15.0 and 16.7,
+// 2,048 of 8 24.5 and 28.2.
 vx_status plan_quant(const vx_geometry *g, int32_t k, int32_t num_splits, Plan *p) {
     VX_TRY(plan(g, k, num_splits, p, vx::quant_warps(g->num_q_heads / g->num_kv_heads), true));
     int sms = 0;
