@@ -245,7 +245,9 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
             for (int e = 0; e < 4; ++e) p[e] *= r[e & 1];
             if (T == 1 && far) {
                 const uint32_t bits = __float_as_uint(tile[t].vs), field = (bits >> 23) & 0xffu;
-                const float mant = field ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : tile[t].vs * 0x1p126f;
+                float mant = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
+                if (field == 0u) mant = tile[t].vs * 0x1p126f;
+                if (field == 255u) mant = tile[t].vs;  // an infinite scale or a NaN shows in the output
                 const float by = static_cast<float>(static_cast<int>(max(field, 1u)) - 127) + DQ_PSHIFT;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - o_run[nt][e & 1] + by) * mant;

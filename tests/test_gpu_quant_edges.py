@@ -313,3 +313,73 @@ def test_tiny_queries_under_large_key_scales(fmt):
     sel = sel[:, :, :5]
     check_mixed(*decode(c, cache, q.to(DEV), dev(sel), sm_scale=2.0 ** -12), attend_mixed(c, q.double().numpy(), sel, 2.0 ** -12))
     assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 40])
+def test_a_scale_that_is_no_number_shows_in_its_row_alone(bad, tiles):
+    c = Case("int8", [16 * tiles, 16 * tiles], 4, 2, 64, 16, seed=37).fill()
+    c.vs[c.idx[c.ptr[0] + tiles // 2], 1] = bad
+    q, sel, cache = c.queries(), c.select(tiles), c.cache()
+    for splits in (0, 1, 3):
+        out, lse = decode(c, cache, q.to(DEV), dev(sel), num_splits=splits)
+        assert not bool(torch.isfinite(out[0, 2:]).any()) and bool(torch.isfinite(out[0, :2]).all())
+        assert bool(torch.isfinite(out[1]).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_appending_step_captured_and_replayed(fmt):
+    """A graph of the quantising append and the chained step, replayed as the tokens, queries and lengths change: bit for bit
+    what the calls give outside of a graph."""
+    B, Hq, Hkv, D, P, k, steps = 3, 8, 4, 128, 16, 6, 20
+    c = Case(fmt, [300, 40, 16 + steps], Hq, Hkv, D, P, seed=43).fill()
+    for s in (c.ks, c.vs):
+        s[:] = 2.0 ** np.rint(np.log2(s))
+    lens = dev(c.L - steps)
+    state = [(c.cache(), torch.randn(c.pool, Hkv, D, generator=torch.Generator(DEV).manual_seed(1), device=DEV).to(torch.bfloat16))
+             for _ in range(2)]
+    kn, vn, q = (torch.zeros(B, h, D, dtype=torch.bfloat16, device=DEV) for h in (Hkv, Hkv, Hq))
+    ws = torch.empty(vx.vx_workspace_size(c.geo, c.max_pages, k), dtype=torch.uint8, device=DEV)
+    outs = [(torch.zeros(B, Hq, D, dtype=torch.bfloat16, device=DEV), torch.zeros(B, Hq, device=DEV)) for _ in range(2)]
+    t = vx.PageTable(c.table.page_ptr, c.table.page_indices, lens, c.max_pages)
+
+    def step(i):
+        vx.vx_block_topk_decode_append_quant(c.geo, t, q, *state[i], kn, vn, k, outs[i][0], ws, lse=outs[i][1], err=c.err)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(0)
+    for _ in range(steps):
+        lens.add_(1)
+        kn.copy_(new_rows(c, B, 2))
+        vn.copy_(new_rows(c, B, 2))
+        q.copy_(c.queries())
+        ws.random_(0, 256)
+        graph.replay()
+        step(1)
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        (a, ca), (b, cb) = state
+        assert torch.equal(ca, cb) and torch.equal(a.k_cache.view(torch.uint8), b.k_cache.view(torch.uint8))
+        assert torch.equal(a.v_cache.view(torch.uint8), b.v_cache.view(torch.uint8))
+        for x, y in ((a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
+            assert torch.equal(x.nan_to_num(), y.nan_to_num())
+    assert int(c.err.item()) == 0 and bool(torch.isfinite(outs[0][0]).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lo,hi", [(-8, -4), (-60, 30)])
+def test_scales_of_both_signs(fmt, lo, hi):
+    """Scales are any finite numbers: negative key and value scales, some zero."""
+    c = Case(fmt, [16, 700, 333], 12, 2, 128, 16, seed=41).fill()
+    sign = lambda: c.rng.choice([-1.0, 1.0], c.ks.shape)
+    c.ks[:] = sign() * 2.0 ** c.rng.integers(-8, -5, c.ks.shape)
+    c.vs[:] = sign() * 2.0 ** c.rng.integers(lo, hi, c.vs.shape) * c.rng.uniform(1, 2, c.vs.shape)
+    c.ks[c.rng.random(c.ks.shape) < 0.1] = 0
+    q, cache = c.queries(), c.cache()
+    for k in (5, 44):
+        sel = c.select(k)
+        want = attend_mixed(c, q.double().numpy(), sel, 1 / np.sqrt(128))
+        for splits in (0, 1, 7):
+            check_mixed(*decode(c, cache, q.to(DEV), dev(sel), num_splits=splits), want)
+    assert int(c.err.item()) == 0
