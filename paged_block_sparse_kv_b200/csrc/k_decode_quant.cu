@@ -34,9 +34,9 @@
 // conversions are hidden: with none at all (a timing copy) 256 requests took 0.5% and 32 requests 0.3%
 // less.  16 warps per SM because a tile is a chain of short steps: 8 warps took 137 us where 16 took
 // 108; the ring then holds 3 tiles per warp, the same 192 KB.  Units that follow the weights (see
-// attend_codes) and partials divided by their sums cost 256 requests 1.5% and 32 requests 1.3%; an
-// integer exponent as the unit took 107.5 us where this takes 106.3, weights computed ahead of the
-// maximum 108.2.
+// attend_codes) and partials divided by their sums cost 256 requests 0.6% and 32 requests 1.0%, in turn
+// with the largest v_scale as the unit (102.3 us there); an integer exponent as the unit cost 2.8%,
+// weights computed ahead of the maximum 3%.
 // Measured and not kept: the block joining its warps' partials itself (its loads of fresh partials
 // cost 4-5 us at the block's end: 37.5 and 33.0 us), the first two tiles issued before the rest (33.3
 // and 32.7), the selection's lines prefetched before the dependency wait (34.9 and 32.7).
@@ -144,19 +144,20 @@ struct Spread {
 // T 16-token tiles of one row.  qf: the query heads as mma B fragments in the dims order above; hs:
 // the logits' scale of heads 2 q4, 2 q4 + 1 (log2 units).  Weights are exp2(logit - m_run) and l_run is
 // their sum; m_run stays up to DQ_MLAG behind the largest logit.  acc: the output, unnormalised, in
-// units of 2^(o_run - DQ_PSHIFT), where o_run is the largest logit + log2 of v_scale met: P is
-// multiplied by v_scale * unit, unit = 2^(m_run - o_run + DQ_PSHIFT), before it is rounded to fp16, so acc
-// needs no multiplication per tile.  What that rounding loses is at most 2^-35 of the largest weight
-// times v_scale met, whatever the scales of the row's pages are: in units of the largest v_scale alone,
-// all of a page was lost that carries the weight under a scale 2^-42 of another's.  (Of a pair, o_run
-// follows the larger scale: 4 bits of 2^-40, and the scale's rounding to a power of two one.)  far: a
-// weight or the unit may leave fp32's range, because the row's scales differ by more than 2^60 or one is
-// below 2^-100: then weight and scale share one exponent.  Two tiles at a time share the maximum's
-// shuffles and give the scheduler two independent chains.
+// units of 2^(m_run + d_run - DQ_PSHIFT), where m_run + d_run is the largest logit + log2 of v_scale
+// met (kept as the difference d_run: beside a logit of 2^24 the sum would be off by whole powers of
+// two, and P out of fp16's range).  P is multiplied by v_scale * unit, unit = 2^(DQ_PSHIFT - d_run),
+// before it is rounded to fp16, so acc needs no multiplication per tile.  What that rounding loses is at
+// most 2^-35 of the largest weight times v_scale met, whatever the scales of the row's pages are: in
+// units of the largest v_scale alone, all of a page was lost that carries the weight under a scale 2^-42
+// of another's.  (Of a pair, d_run follows the larger scale: 4 bits of 2^-40, and the scale's rounding to
+// a power of two one.)  far: a weight or the unit may leave fp32's range, because the row's scales differ
+// by more than 2^60 or one is below 2^-100: then weight and scale share one exponent.  Two tiles at a
+// time share the maximum's shuffles and give the scheduler two independent chains.
 template <int D, int NT, int FMT, int T>
 __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32_t (&qf)[NT][D / 16][2],
                                              const float (&hs)[NT][2], float (&acc)[NT][D / 16][4],
-                                             float (&m_run)[NT][2], float (&l_run)[NT][2], float (&o_run)[NT][2],
+                                             float (&m_run)[NT][2], float (&l_run)[NT][2], float (&d_run)[NT][2],
                                              float (&unit)[NT][2], bool far, int lane) {
     constexpr int MT = D / 16;
     constexpr int HALVES = D / 64;  // 16-byte chunks a lane takes of a token row
@@ -196,7 +197,7 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
     uint32_t pb[T][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float x[T][4], m_new[2], o_new[2];
+        float x[T][4], most[2];
         bool change = false;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -213,19 +214,21 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-            const float top = mx + ve;
-            m_new[i] = mx > m_run[nt][i] + DQ_MLAG ? mx : m_run[nt][i];
-            o_new[i] = fmaxf(o_run[nt][i], top);
-            change |= mx > m_run[nt][i] + DQ_MLAG || top > o_run[nt][i];
+            most[i] = mx;
+            const float above = mx - m_run[nt][i];
+            change |= above > DQ_MLAG || above + ve > d_run[nt][i];
         }
         if (__any_sync(FULL, change)) {  // rare after a row's first tiles
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float alpha = exp2f(o_run[nt][i] - o_new[i]);
-                l_run[nt][i] *= exp2f(m_run[nt][i] - m_new[i]);
-                unit[nt][i] = exp2f(m_new[i] - o_new[i] + DQ_PSHIFT);
-                m_run[nt][i] = m_new[i];
-                o_run[nt][i] = o_new[i];
+                const float m = most[i] - m_run[nt][i] > DQ_MLAG ? most[i] : m_run[nt][i];
+                const float by = m_run[nt][i] - m;  // 0, or -inf at a row's first tiles
+                const float d = fmaxf(d_run[nt][i] + by, most[i] - m + ve);
+                const float alpha = exp2f(d_run[nt][i] + by - d);
+                l_run[nt][i] *= exp2f(by);
+                unit[nt][i] = exp2f(DQ_PSHIFT - d);
+                m_run[nt][i] = m;
+                d_run[nt][i] = d;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     acc[nt][mt][i] *= alpha;
@@ -250,7 +253,7 @@ __device__ __forceinline__ void attend_codes(const Tile (&tile)[T], const uint32
                 if (field == 255u) mant = tile[t].vs;  // an infinite scale or a NaN shows in the output
                 const float by = static_cast<float>(static_cast<int>(max(field, 1u)) - 127) + DQ_PSHIFT;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - o_run[nt][e & 1] + by) * mant;
+                for (int e = 0; e < 4; ++e) p[e] = exp2f(x[t][e] - m_run[nt][e & 1] + (by - d_run[nt][e & 1])) * mant;
             }
             pb[t][nt][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
             pb[t][nt][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
     uint32_t qf[NT][MT][2];
     float hs[NT][2];
     float acc[NT][MT][4];
-    float m_run[NT][2], l_run[NT][2], o_run[NT][2], unit[NT][2];
+    float m_run[NT][2], l_run[NT][2], d_run[NT][2], unit[NT][2];
 
     // partial of row `r` (at least one tile attended) for piece `c`: slot r + c.  The output is divided
     // by its sum before its unit goes in: no number is then larger than the largest value
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
                 if (head < a.G) {
                     float *o = a.o_part + (slot * a.G + head) * D + 2 * g4;
                     const float inv = v > 0.f ? __fdividef(DQ_PUNIT, v) : 0.f;
-                    const float half = exp2f(0.5f * (o_run[nt][i] - m_run[nt][i]));  // the unit can be 2^128
+                    const float half = exp2f(0.5f * d_run[nt][i]);  // the unit can be 2^128
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
                         *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * half * half,
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m_run[nt][i] = o_run[nt][i] = -INFINITY;
+                m_run[nt][i] = d_run[nt][i] = -INFINITY;
                 l_run[nt][i] = unit[nt][i] = 0.f;
             }
 #pragma unroll
@@ -550,10 +553,10 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
         spread.next(tile[0].vs, tile[1].vs, pair, far);
         if (!pair) count = 1;  // the second one waits for the next round
         if (count == 2) {
-            attend_codes<D, NT, FMT, 2>(tile, qf, hs, acc, m_run, l_run, o_run, unit, false, lane);
+            attend_codes<D, NT, FMT, 2>(tile, qf, hs, acc, m_run, l_run, d_run, unit, false, lane);
         } else {
             const Tile one[1] = {tile[0]};
-            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, o_run, unit, far, lane);
+            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, d_run, unit, far, lane);
         }
         attended = true;
         __syncwarp();  // every lane is done with these stages before they are refilled
@@ -758,12 +761,12 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
     }
     const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
     uint32_t qf[NT][MT][2];
-    float hs[NT][2], acc[NT][MT][4], m_run[NT][2], l_run[NT][2], o_run[NT][2], unit[NT][2];
+    float hs[NT][2], acc[NT][MT][4], m_run[NT][2], l_run[NT][2], d_run[NT][2], unit[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            m_run[nt][i] = o_run[nt][i] = -INFINITY;
+            m_run[nt][i] = d_run[nt][i] = -INFINITY;
             l_run[nt][i] = unit[nt][i] = 0.f;
         }
 #pragma unroll
@@ -796,10 +799,10 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
         bool pair, far;
         spread.next(t0.vs, two[1].vs, pair, far);
         if (others && pair) {
-            attend_codes<D, NT, FMT, 2>(two, qf, hs, acc, m_run, l_run, o_run, unit, false, lane);
+            attend_codes<D, NT, FMT, 2>(two, qf, hs, acc, m_run, l_run, d_run, unit, false, lane);
         } else {
             const Tile one[1] = {t0};
-            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, o_run, unit, far, lane);
+            attend_codes<D, NT, FMT, 1>(one, qf, hs, acc, m_run, l_run, d_run, unit, far, lane);
             left = others;  // the second one waits for the next round
         }
     }
@@ -819,7 +822,7 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
             }
             if (head < a.G && valid) {  // divided by its sum, as in k_decode_quant
                 float *o = s_o + (warp * a.G + head) * D + 2 * g4;
-                const float inv = v > 0.f ? __fdividef(DQ_PUNIT, v) : 0.f, half = exp2f(0.5f * (o_run[nt][i] - m_run[nt][i]));
+                const float inv = v > 0.f ? __fdividef(DQ_PUNIT, v) : 0.f, half = exp2f(0.5f * d_run[nt][i]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     *reinterpret_cast<float2 *>(o + mt * 16) = make_float2(acc[nt][mt][i] * inv * half * half,

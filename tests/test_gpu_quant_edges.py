@@ -383,3 +383,25 @@ def test_scales_of_both_signs(fmt, lo, hi):
         for splits in (0, 1, 7):
             check_mixed(*decode(c, cache, q.to(DEV), dev(sel), num_splits=splits), want)
     assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [1e4, 1e7, 1e9, 1e20, 1e30])
+@pytest.mark.parametrize("k", [7, 40])
+def test_large_logits_stay_a_mean_of_values(fmt, size, k):
+    """Logits so large that fp32 has no digits left behind the point, beside ordinary value scales: the output is still a mean
+    of the row's values, so no larger than the largest."""
+    c = Case(fmt, [16, 640, 333], 8, 2, 64, 16, seed=47).fill()
+    c.vs[:] = 2.0 ** c.rng.integers(-9, 9, c.vs.shape) * c.rng.uniform(1, 2, c.vs.shape)
+    q, cache = c.queries(), c.cache()
+    sel = c.select(k)
+    values = c.float_values()[1]
+    for splits in (0, 1, 5):
+        out, lse = decode(c, cache, q.to(DEV), dev(sel), num_splits=splits, sm_scale=size)
+        assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+        for b in range(3):
+            for h in range(2):
+                top = np.max([np.abs(values[c.idx[c.ptr[b] + j], h, :min(16, c.L[b] - 16 * j)]).max((0,)) for j in sel[b, h]
+                              if j >= 0], axis=0)
+                got = out[b, 4 * h:4 * h + 4].double().abs().cpu().numpy()
+                assert (got <= top * (1 + 2.0 ** -7)).all()
