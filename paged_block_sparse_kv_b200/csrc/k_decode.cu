@@ -416,10 +416,10 @@ __global__ void __launch_bounds__(256) k_merge(const DecodeArgs a) {
     if (item >= rows * a.G * NSLICE) return;
     const int slice = static_cast<int>(item % NSLICE);
     const int64_t rg = item / NSLICE;
-    const int64_t r = div64(rg, a.G);
+    const int64_t r = div_units<NORMALISED>(rg, a.G);
     const int g = static_cast<int>(rg - r * a.G);
-    const int64_t c_lo = piece_of(r * a.units_per_row, a.units, a.static_units, a.static_chunks, a.chunks);
-    const int64_t c_hi = piece_of((r + 1) * a.units_per_row - 1, a.units, a.static_units, a.static_chunks, a.chunks);
+    const int64_t c_lo = piece_of<NORMALISED>(r * a.units_per_row, a.units, a.static_units, a.static_chunks, a.chunks);
+    const int64_t c_hi = piece_of<NORMALISED>((r + 1) * a.units_per_row - 1, a.units, a.static_units, a.static_chunks, a.chunks);
     const int np = static_cast<int>(c_hi - c_lo + 1);
     const float *ml0 = a.ml_part + ((r + c_lo) * a.G + g) * 2;                               // partial i at + i*G*2
     const float *o0 = a.o_part + ((r + c_lo) * a.G + g) * DV + slice * SLICE + lane * PER;   // partial i at + i*G*DV

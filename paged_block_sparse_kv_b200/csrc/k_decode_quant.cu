@@ -28,14 +28,14 @@
 // Value codes past the request's length are zeroed in registers, logits there are -inf.
 //
 // Bound: HBM (2 bytes read per token, KV head and dim for 4 G operations).  Measured on one B200,
-// whole call: 256 requests of 64 pages (543 MB) 105 us, 5.2 TB/s, the decode kernel alone 5.5 TB/s;
+// whole call: 256 requests of 64 pages (543 MB) 103-107 us by the GPU, 5.1-5.3 TB/s, the decode kernel alone 5.5 TB/s;
 // 32 requests of 128 pages (135 MB) 33.5 us, 4.0 TB/s: 3 us until the first copies leave (selection,
 // then page table, both from DRAM), warps that end over 9 us (22 to 31 us), the merge.  The
 // conversions are hidden: with none at all (a timing copy) 256 requests took 0.5% and 32 requests 0.3%
 // less.  16 warps per SM because a tile is a chain of short steps: 8 warps took 137 us where 16 took
 // 108; the ring then holds 3 tiles per warp, the same 192 KB.  Units that follow the weights (see
-// attend_codes) and partials divided by their sums cost 256 requests 0.6% and 32 requests 1.0%, in turn
-// with the largest v_scale as the unit (102.3 us there); an integer exponent as the unit cost 2.8%,
+// attend_codes) and partials divided by their sums cost 256 requests 0.6 to 1.8% (by the GPU) and 32
+// requests 1.2%, in turn with the largest v_scale as the unit; an integer exponent as the unit cost 2.8%,
 // weights computed ahead of the maximum 3%.
 // Measured and not kept: the block joining its warps' partials itself (its loads of fresh partials
 // cost 4-5 us at the block's end: 37.5 and 33.0 us), the first two tiles issued before the rest (33.3
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
         }
     };
     auto p_start = [&](int64_t c) -> int64_t {
-        if constexpr (LATE) return piece_start(c, a.units, a.static_units, a.static_chunks, a.chunks);
-        return chunk_start(c, a.units, a.chunks);
+        if constexpr (LATE) return piece_start<true>(c, a.units, a.static_units, a.static_chunks, a.chunks);
+        return chunk_start<true>(c, a.units, a.chunks);
     };
     // the next piece this warp takes after its static one (warp-uniform): from the counter, or
     // round robin over the warps; a.chunks or more: none left
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(quant_warps(NT * 8) * 32, 1)
 
     Resolved rs;
     auto resolve = [&]() {
-        rs = resolve_unit(a, batch + lane, f_end);
+        rs = resolve_unit<true>(a, batch + lane, f_end);
         return __ballot_sync(FULL, rs.valid);
     };
     uint32_t pending = resolve();
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(256) k_merge_many(const DecodeArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x;
     const int g = blockIdx.y;
-    auto piece = [&](int64_t u) { return piece_of(u, a.units, a.static_units, a.static_chunks, a.chunks); };
+    auto piece = [&](int64_t u) { return piece_of<true>(u, a.units, a.static_units, a.static_chunks, a.chunks); };
     const int64_t lo = piece(r * a.units_per_row);
     const int n = static_cast<int>(piece((r + 1) * a.units_per_row - 1) - lo + 1);
     Joined<D> j;
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(256, 6) k_merge_few(const DecodeArgs a) {
     const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t r = item / (uint32_t)a.G, g = item - r * (uint32_t)a.G;
     if (r >= (uint32_t)a.B * (uint32_t)a.Hkv) return;
-    auto piece = [&](int64_t u) { return piece_of(u, a.units, a.static_units, a.static_chunks, a.chunks); };
+    auto piece = [&](int64_t u) { return piece_of<true>(u, a.units, a.static_units, a.static_chunks, a.chunks); };
     const int64_t lo = piece((int64_t)r * a.units_per_row);
     const int n = static_cast<int>(piece(((int64_t)r + 1) * a.units_per_row - 1) - lo + 1);
     using J = Joined<D>;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(WARPS * 32, quant_warps(NT * 8) / WARPS)
     const int64_t u = (int64_t)((lane >> 1) * WARPS + warp) * 2 + (lane & 1);
     Resolved rs{0, 0, 0, 0, false};
     if (lane < SLOTS && u < a.units_per_row)
-        rs = resolve_unit(a, r * a.units_per_row + u, (r + 1) * a.units_per_row);
+        rs = resolve_unit<true>(a, r * a.units_per_row + u, (r + 1) * a.units_per_row);
     const uint32_t valid = __ballot_sync(FULL, rs.valid);
     float ks = 0.f, vs = 0.f;
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(valid) * 2 * TILE_BYTES);

@@ -13,12 +13,13 @@
 namespace vx {
 
 // Unit u of the flat tile list (invalid past u_end, for an empty slot or a bad entry).
+template <bool NARROW = false>
 __device__ __forceinline__ Resolved resolve_unit(const DecodeArgs &a, int64_t u, int64_t u_end) {
     Resolved rs{0, 0, 0, 0, false};
     if (u >= u_end) return rs;
-    const int64_t r = div64(u, a.units_per_row);
+    const int64_t r = div_units<NARROW>(u, a.units_per_row);
     const int64_t rem = u - r * a.units_per_row;
-    const int i = static_cast<int>(div64(rem, a.tiles_per_page));
+    const int i = static_cast<int>(div_units<NARROW>(rem, a.tiles_per_page));
     const int sub = static_cast<int>(rem - (int64_t)i * a.tiles_per_page);
     const int b = static_cast<int>((uint32_t)r / (uint32_t)a.Hkv), h = static_cast<int>((uint32_t)r % (uint32_t)a.Hkv);
     rs.row = static_cast<int32_t>(r);
